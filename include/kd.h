@@ -209,6 +209,74 @@ int kd_decode_noalloc(kd_ctx *ctx, const int32_t *d_tokens, int32_t n_tokens, in
  * NULL turns tracing off. */
 int kd_set_trace(kd_ctx *ctx, unsigned long long *d_buf, int64_t n_words, int32_t every);
 
+/* ------------------------------------------------------------------------------------------
+ * Prompt operators: the products and the attention of a layer for many tokens at once (or one),
+ * on the tensor cores. They need no handle: inputs and outputs are device memory of the current
+ * CUDA device, `stream` is a cudaStream_t (NULL: the legacy default stream), every call only
+ * enqueues work there and allocates nothing. Calls on different streams and from different host
+ * threads do not touch each other, and all may be captured into a CUDA graph. Sums, softmax
+ * statistics and epilogues are fp32; inputs are bf16 or fp16 and outputs are rounded once, to
+ * nearest. Results do not vary from run to run.
+ *
+ * Arguments are checked on the host before anything is enqueued: KD_EINVAL, KD_ENOMEM (a
+ * workspace too small) or KD_ECUDA, with the text in kd_op_error() (of the calling thread).
+ * A matrix that is an input of a product (x, w, wg, wu) starts on 16 bytes and has rows a
+ * multiple of 8 elements apart; any other matrix needs only its element's alignment. Strides
+ * (ld_*) count elements between the starts of rows; the stride of a single row is not used.
+ * Outputs must not overlap inputs, except that `residual` may be `out` itself. */
+enum { KD_BF16 = 0, KD_F16 = 1, KD_F32 = 2 };
+/* Activations: z; max(z, 0); z / (1 + e^-z); z (1 + erf(z / sqrt 2)) / 2. */
+enum { KD_ACT_NONE = 0, KD_ACT_RELU = 1, KD_ACT_SILU = 2, KD_ACT_GELU = 3 };
+
+/* out[m][n] = residual[m][n] + act(sum_k x[m][k] w[n][k] + bias[n]).
+ * dtype: of x, w and bias (KD_BF16, KD_F16). out_dtype: of residual and out (dtype or KD_F32).
+ * w_transposed: w is laid out [k][n] instead of [n][k]. bias, residual: may be NULL.
+ * m and n may be 0 (nothing is done); k >= 1. */
+typedef struct kd_linear_args {
+    int32_t dtype, out_dtype, act, w_transposed;
+    int64_t m, n, k;
+    const void *x;
+    int64_t ld_x;
+    const void *w;
+    int64_t ld_w;
+    const void *bias;
+    const void *residual;
+    int64_t ld_residual;
+    void *out;
+    int64_t ld_out;
+} kd_linear_args;
+int kd_linear(const kd_linear_args *args, void *stream);
+
+/* The gated feed-forward block up to its product: g = x wg^T, u = x wu^T, h = act(g) * u, for
+ * m tokens of d elements and f hidden units; x [m][d], wg and wu [f][d] (weights interleaved
+ * row by row are two matrices of stride 2 d), h [m][f], all of one type. m, f may be 0. */
+typedef struct kd_gated_args {
+    int32_t dtype, act;
+    int64_t m, d, f;
+    const void *x;
+    int64_t ld_x;
+    const void *wg;
+    int64_t ld_wg;
+    const void *wu;
+    int64_t ld_wu;
+} kd_gated_args;
+int kd_gated_ffn(const kd_gated_args *args, void *h, int64_t ld_h, void *stream);
+
+/* Its gradients for a given dh [m][f]: dx [m][d] (sum of both projections' shares), dwg and dwu
+ * [f][d], of the inputs' type; NULL skips one. g and u are recomputed; their gradients are held
+ * in the workspace in the inputs' type. m, f >= 1. */
+size_t kd_gated_ffn_backward_workspace(int64_t m, int64_t f);
+int kd_gated_ffn_backward(const kd_gated_args *args, const void *dh, int64_t ld_dh, void *dx, int64_t ld_dx, void *dwg,
+                          int64_t ld_dwg, void *dwu, int64_t ld_dwu, void *workspace, size_t workspace_bytes,
+                          void *stream);
+
+/* Wait for `stream` and report a device-side wait of an operator that ran out of its limit
+ * (2 s; such a kernel ends early and its outputs are not valid): KD_OK or KD_ETIMEOUT, once. */
+int kd_op_sync(void *stream);
+
+/* The text of the calling thread's last operator call that failed. */
+const char *kd_op_error(void);
+
 /* Next KV position to be written (host-side view, valid once calls were enqueued). */
 int32_t kd_position(const kd_ctx *ctx);
 

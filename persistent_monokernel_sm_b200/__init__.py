@@ -15,7 +15,23 @@ import os
 __all__ = ["KdError", "kd_config", "kd_weights", "kd_info", "load_library", "Decoder", "config_from",
            "kd_arena_bytes", "kd_step_bytes", "kd_create", "kd_load_weights", "kd_set_kv", "kd_reset",
            "kd_decode", "kd_generate", "kd_sync", "kd_position", "kd_set_trace", "kd_set_timeout", "kd_set_sampling", "kd_decode_noalloc", "kd_get_info", "kd_kv_ptr",
-           "kd_last_error", "kd_strerror", "kd_destroy", "LIB_PATH", "ERRORS"]
+           "kd_last_error", "kd_strerror", "kd_destroy", "LIB_PATH", "ERRORS",
+           "kd_linear_args", "kd_gated_args", "kd_linear", "kd_gated_ffn", "kd_gated_ffn_backward_workspace",
+           "kd_gated_ffn_backward", "kd_op_sync", "kd_op_error",
+           "linear", "gated_ffn", "gated_ffn_backward"]
+
+_OPERATORS = ("linear", "gated_ffn", "gated_ffn_backward")
+
+
+def __getattr__(name):
+    """The operators on torch tensors; torch is imported when one is first used."""
+    if name not in _OPERATORS:
+        raise AttributeError("module %r has no attribute %r" % (__name__, name))
+    from . import operators
+    for n in _OPERATORS:
+        globals()[n] = getattr(operators, n)
+    return globals()[name]
+
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkd.so")
 
@@ -43,6 +59,21 @@ class kd_info(ctypes.Structure):
                                                "attn_pieces")] + \
                [(n, ctypes.c_int64) for n in ("arena_bytes", "weight_bytes", "kv_bytes", "launches", "ctl_offset")] + \
                [("sync_replicas", ctypes.c_int32), ("sync_offset", ctypes.c_int64 * 2)]
+
+
+class kd_linear_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "out_dtype", "act", "w_transposed")] + \
+               [(n, ctypes.c_int64) for n in ("m", "n", "k")] + \
+               [("x", ctypes.c_void_p), ("ld_x", ctypes.c_int64), ("w", ctypes.c_void_p), ("ld_w", ctypes.c_int64),
+                ("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("ld_residual", ctypes.c_int64),
+                ("out", ctypes.c_void_p), ("ld_out", ctypes.c_int64)]
+
+
+class kd_gated_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "act")] + \
+               [(n, ctypes.c_int64) for n in ("m", "d", "f")] + \
+               [("x", ctypes.c_void_p), ("ld_x", ctypes.c_int64), ("wg", ctypes.c_void_p), ("ld_wg", ctypes.c_int64),
+                ("wu", ctypes.c_void_p), ("ld_wu", ctypes.c_int64)]
 
 
 class KdError(RuntimeError):
@@ -85,6 +116,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "kd_last_error": (ctypes.c_char_p, [_P]),
         "kd_strerror": (ctypes.c_char_p, [ctypes.c_int]),
         "kd_destroy": (None, [_P]),
+        # the argument structs of the operators are taken as a pointer or as packed bytes
+        "kd_linear": (ctypes.c_int, [ctypes.c_char_p, _P]),
+        "kd_gated_ffn": (ctypes.c_int, [ctypes.c_char_p, _P, ctypes.c_int64, _P]),
+        "kd_gated_ffn_backward_workspace": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64]),
+        "kd_gated_ffn_backward": (ctypes.c_int, [ctypes.c_char_p] + [_P, ctypes.c_int64] * 4 + [_P, ctypes.c_size_t, _P]),
+        "kd_op_sync": (ctypes.c_int, [_P]),
+        "kd_op_error": (ctypes.c_char_p, []),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -188,6 +226,39 @@ def kd_strerror(code: int) -> str:
 
 def kd_destroy(h) -> None:
     load_library().kd_destroy(h)
+
+
+def _check_op(rc, what):
+    if rc:
+        raise KdError(rc, "%s: %s" % (what, kd_op_error()))
+    return rc
+
+
+def kd_linear(args: kd_linear_args, stream: int | None) -> int:
+    return _check_op(load_library().kd_linear(bytes(args), stream), "kd_linear")
+
+
+def kd_gated_ffn(args: kd_gated_args, h: int, ld_h: int, stream: int | None) -> int:
+    return _check_op(load_library().kd_gated_ffn(bytes(args), h, ld_h, stream), "kd_gated_ffn")
+
+
+def kd_gated_ffn_backward_workspace(m: int, f: int) -> int:
+    return load_library().kd_gated_ffn_backward_workspace(m, f)
+
+
+def kd_gated_ffn_backward(args: kd_gated_args, dh: int, ld_dh: int, dx: int | None, ld_dx: int, dwg: int | None,
+                          ld_dwg: int, dwu: int | None, ld_dwu: int, workspace: int, workspace_bytes: int,
+                          stream: int | None) -> int:
+    return _check_op(load_library().kd_gated_ffn_backward(bytes(args), dh, ld_dh, dx, ld_dx, dwg, ld_dwg, dwu, ld_dwu,
+                                                          workspace, workspace_bytes, stream), "kd_gated_ffn_backward")
+
+
+def kd_op_sync(stream: int | None) -> int:
+    return _check_op(load_library().kd_op_sync(stream), "kd_op_sync")
+
+
+def kd_op_error() -> str:
+    return (load_library().kd_op_error() or b"").decode()
 
 
 # ---------------------------------------------------------------- convenience

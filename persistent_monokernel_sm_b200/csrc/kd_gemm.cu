@@ -1,0 +1,717 @@
+// kd_gemm.cu -- the batched products of a layer on the 5th-generation tensor cores: linear
+// (bias, activation, residual in the epilogue), the gated feed-forward block and its gradients.
+//
+// One kernel computes D[n][t] = sum_k A[n][k] B[t][k]: A is the weight side, whose index n is
+// the contiguous one of the output, B the token side. Tensor memory then holds an output
+// feature per lane and a token per column, so that
+//  * a bias is one register per thread, and 32 lanes write 32 neighbouring outputs of a token;
+//  * few tokens (one, at serving) cost few columns: the tile is 128 features x 16 tokens there,
+//    and the tensor core streams weights at the rate of HBM;
+//  * the gated block's gate and up rows of one feature lie 16 lanes apart (its A tile takes 16
+//    gate rows, 16 up rows, 16 gate rows ...), so act(g) * u is one shuffle per column pair.
+//
+// Structure: one CTA per SM loops over output tiles. A producer thread fills a ring of 64-deep
+// k-blocks by TMA (128-byte swizzle), one thread issues tcgen05.mma, eight warps read the
+// accumulators out of tensor memory, which holds two tiles so that the products of the next one
+// run meanwhile. With few tiles the reduction is split over the CTAs of a cluster, whose
+// partial tiles are summed in rank order through distributed shared memory: no workspace, one
+// launch, the same result every time.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdarg.h>
+#include <stdio.h>
+#include <string.h>
+
+#include <atomic>
+
+#include "kd.h"
+#include "kd_layout.h"
+#include "kd_ops.h"
+#include "kd_sm100.h"
+
+namespace kd {
+
+// ------------------------------------------------------------------ host helpers
+static thread_local char t_err[512];
+
+int op_fail(int code, const char* fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(t_err, sizeof t_err, fmt, ap);
+    va_end(ap);
+    return code;
+}
+
+int op_sm_count(int* sms) {
+    static std::atomic<int> cached[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return op_fail(KD_ECUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
+    int n = dev < 64 ? cached[dev].load() : 0;
+    if (n == 0) {
+        e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return op_fail(KD_ECUDA, "cudaDeviceGetAttribute: %s", cudaGetErrorString(e));
+        if (dev < 64) cached[dev].store(n);
+    }
+    *sms = n;
+    return KD_OK;
+}
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static EncodeFn encode_fn() {
+    static std::atomic<void*> fn{nullptr};
+    void* f = fn.load();
+    if (!f) {
+        cudaDriverEntryPointQueryResult st;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &st) != cudaSuccess ||
+            st != cudaDriverEntryPointSuccess)
+            return nullptr;
+        fn.store(f);
+    }
+    return (EncodeFn)f;
+}
+
+static int encode(CUtensorMap* m, int dtype, const void* base, int rank, const cuuint64_t* dims,
+                  const cuuint64_t* strides, const cuuint32_t* box) {
+    EncodeFn f = encode_fn();
+    if (!f) return op_fail(KD_ECUDA, "the driver has no cuTensorMapEncodeTiled");
+    const cuuint32_t ones[3] = {1, 1, 1};
+    const CUresult r = f(m, dtype == KD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                         (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, ones,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return op_fail(KD_ECUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return KD_OK;
+}
+
+int make_map_2d(CUtensorMap* m, int dtype, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_cols,
+                int box_rows) {
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+    return encode(m, dtype, base, 2, dims, strides, box);
+}
+
+int make_map_3d(CUtensorMap* m, int dtype, const void* base, int64_t c0, int64_t c1, int64_t c2, int64_t ld1,
+                int64_t ld2, int box0, int box1, int box2) {
+    const cuuint64_t dims[3] = {(cuuint64_t)c0, (cuuint64_t)c1, (cuuint64_t)c2};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld1 * 2, (cuuint64_t)ld2 * 2};
+    const cuuint32_t box[3] = {(cuuint32_t)box0, (cuuint32_t)box1, (cuuint32_t)box2};
+    return encode(m, dtype, base, 3, dims, strides, box);
+}
+
+namespace {
+
+constexpr int kGemmThreads = 320;  // 8 epilogue warps, the producer's warp, the issuer's warp
+constexpr int kBK = 64;            // k-block: 128 bytes of a row
+constexpr int kABytes = 128 * kBK * 2;
+constexpr int kMaxRing = 12;
+constexpr int kRingBytes = 216 * 1024;
+constexpr int kGroup = 8;  // token tiles that are taken together while the weight tiles advance
+
+enum { EPI_LINEAR = 0, EPI_GATED = 1, EPI_GATED_BWD = 2 };
+
+struct GemmArgs {
+    int n_tiles, t_tiles;  // tiles over features and tokens
+    int kb0, kb;           // k-blocks of the first operand pair, of both
+    int bn, stages, splits;
+    int a_mn, b_mn;
+    uint32_t idesc;
+    int act;
+    int64_t N, M;  // features (of the output), tokens
+    const void* bias;
+    const void* res;  // residual; the backward pass's dh
+    int64_t ld_res;
+    void* out;
+    void* out2;  // the backward pass's du
+    int64_t ld_out;
+};
+
+// ------------------------------------------------------------------ activations
+// fp32 throughout; silu and its slope by the fast exponential (2 ulp).
+template <int ACT>
+__device__ __forceinline__ float act_fn(float z) {
+    if constexpr (ACT == KD_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
+    if constexpr (ACT == KD_ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
+    if constexpr (ACT == KD_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+    return z;
+}
+template <int ACT>
+__device__ __forceinline__ void act_slope(float z, float* a, float* s) {
+    if constexpr (ACT == KD_ACT_RELU) {
+        *a = z > 0.f ? z : (z != z ? z : 0.f);
+        *s = z > 0.f ? 1.f : 0.f;
+    } else if constexpr (ACT == KD_ACT_SILU) {
+        const float p = __fdividef(1.f, 1.f + __expf(-z));
+        *a = z * p;
+        *s = p * (1.f + z * (1.f - p));
+    } else if constexpr (ACT == KD_ACT_GELU) {
+        const float c = 0.5f * (1.f + erff(z * 0.70710678118654752f));
+        *a = z * c;
+        *s = c + z * 0.39894228040143268f * __expf(-0.5f * z * z);
+    } else {
+        *a = z;
+        *s = 1.f;
+    }
+}
+
+// ------------------------------------------------------------------ epilogue
+template <typename T> __device__ __forceinline__ float to_f(T v) { return Half2<T>::up(v); }
+template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }
+template <typename T> __device__ __forceinline__ T from_f(float v) { return Half2<T>::down(v); }
+template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
+
+// COLS columns (tokens t0 ...) of this warp's 32 lanes. `quad`: which 32 rows of the tile.
+template <int EPI, int ACT, int COLS, typename T, typename O>
+__device__ __forceinline__ void emit(const GemmArgs& g, const float* v, int64_t tile_n, int quad, int lane, int64_t t0,
+                                     float bias) {
+    const int64_t left = g.M - t0;  // tokens of this block that exist
+    if constexpr (EPI == EPI_LINEAR) {
+        const int64_t n = tile_n * 128 + quad * 32 + lane;
+        const bool in = n < g.N;
+        O* out = (O*)g.out + t0 * g.ld_out + n;
+        float r[COLS];
+        if (g.res) {
+            const O* res = (const O*)g.res + t0 * g.ld_res + n;
+#pragma unroll
+            for (int j = 0; j < COLS; ++j) r[j] = in && j < left ? to_f<O>(res[j * g.ld_res]) : 0.f;
+        } else {
+#pragma unroll
+            for (int j = 0; j < COLS; ++j) r[j] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < COLS; ++j)
+            if (in && j < left) out[j * g.ld_out] = from_f<O>(act_fn<ACT>(v[j] + bias) + r[j]);
+    } else {
+        const bool low = lane < 16;
+        const int64_t n = tile_n * 64 + quad * 16 + (lane & 15);
+        const bool in = n < g.N;
+        const int64_t at = t0 + (low ? 0 : 1);
+        T dh[COLS / 2];
+        if constexpr (EPI == EPI_GATED_BWD) {
+            const T* p = (const T*)g.res + at * g.ld_res + n;
+#pragma unroll
+            for (int j = 0; j < COLS / 2; ++j)
+                dh[j] = in && at + 2 * j < g.M ? p[2 * j * g.ld_res] : from_f<T>(0.f);
+        }
+#pragma unroll
+        for (int j = 0; j < COLS / 2; ++j) {
+            const float a = v[2 * j], b = v[2 * j + 1];
+            const float got = __shfl_xor_sync(0xffffffffu, low ? b : a, 16);
+            const float gate = low ? a : got, up = low ? got : b;
+            if (!in || at + 2 * j >= g.M) continue;
+            const int64_t o = (at + 2 * j) * g.ld_out + n;
+            if constexpr (EPI == EPI_GATED) {
+                ((T*)g.out)[o] = from_f<T>(act_fn<ACT>(gate) * up);
+            } else {
+                float f, s;
+                act_slope<ACT>(gate, &f, &s);
+                const float d = to_f<T>(dh[j]);
+                ((T*)g.out)[o] = from_f<T>(d * up * s);
+                ((T*)g.out2)[o] = from_f<T>(d * f);
+            }
+        }
+    }
+}
+
+template <int EPI, int COLS, typename T, typename O>
+__device__ __forceinline__ void emit_act(const GemmArgs& g, const float* v, int64_t tile_n, int quad, int lane,
+                                         int64_t t0, float bias) {
+    switch (g.act) {
+        case KD_ACT_RELU: emit<EPI, KD_ACT_RELU, COLS, T, O>(g, v, tile_n, quad, lane, t0, bias); break;
+        case KD_ACT_SILU: emit<EPI, KD_ACT_SILU, COLS, T, O>(g, v, tile_n, quad, lane, t0, bias); break;
+        case KD_ACT_GELU: emit<EPI, KD_ACT_GELU, COLS, T, O>(g, v, tile_n, quad, lane, t0, bias); break;
+        default: emit<EPI, KD_ACT_NONE, COLS, T, O>(g, v, tile_n, quad, lane, t0, bias); break;
+    }
+}
+
+// ------------------------------------------------------------------ the kernel
+template <int EPI, typename T, typename O>
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    gemm_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUtensorMap a1,
+                const __grid_constant__ CUtensorMap b0, const __grid_constant__ CUtensorMap b1,
+                const __grid_constant__ GemmArgs g) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t s_full[kMaxRing], s_empty[kMaxRing], s_tfull[2], s_tempty[2], s_drain;
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int s_dead;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t ring = (smem_u32(smem_raw) + 1023) & ~1023u;
+    const int bbytes = g.bn * kBK * 2, sbytes = kABytes + bbytes;
+    const uint32_t full = smem_u32(s_full), empty = smem_u32(s_empty);
+    const uint32_t tfull = smem_u32(s_tfull), tempty = smem_u32(s_tempty), drain = smem_u32(&s_drain);
+    uint32_t cols = 32;
+    while ((int)cols < 2 * g.bn) cols *= 2;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < g.stages; ++i) mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(tfull + 8 * i, 1), mbar_init(tempty + 8 * i, 8);
+        mbar_init(drain, 1);
+        s_dead = 0;
+        fence_barrier_init();
+    }
+    if (warp == 8 && lane == 0) {
+        tma_prefetch(&a0);
+        tma_prefetch(&b0);
+    }
+    if (warp == 9) tmem_alloc<1>(smem_u32(&s_tmem), cols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    volatile int* dead = &s_dead;
+
+    const int rank = g.splits > 1 ? (int)cluster_rank() : 0;
+    const int first = blockIdx.x / g.splits, step = gridDim.x / g.splits;
+    const int tiles = g.n_tiles * g.t_tiles;
+    const int k_lo = (int)((long long)g.kb * rank / g.splits), k_hi = (int)((long long)g.kb * (rank + 1) / g.splits);
+
+    // Tile order: kGroup token tiles together, weight tiles advancing: the CTAs at work at one
+    // time then share a few token tiles and a few weight tiles, which L2 serves.
+    auto place = [&](int tile, int& tn, int& tt) {
+        const int per = kGroup * g.n_tiles, grp = tile / per, in = tile % per;
+        const int size = min(kGroup, g.t_tiles - grp * kGroup);
+        tn = in / size;
+        tt = grp * kGroup + in % size;
+    };
+
+    if (warp == 8) {  // ---------------------------------------------- producer
+        if (lane == 0) {
+            int it = 0;
+            bool ok = true;
+            for (int tile = first; tile < tiles && ok; tile += step) {
+                int tn, tt;
+                place(tile, tn, tt);
+                for (int kb = k_lo; kb < k_hi; ++kb, ++it) {
+                    const int st = it % g.stages, ph = (it / g.stages) & 1;
+                    if (!(ok = mbar_wait(empty + 8 * st, ph ^ 1, dead))) break;
+                    const uint32_t bar = full + 8 * st, sa = ring + st * sbytes, sb = sa + kABytes;
+                    mbar_expect(bar, sbytes);
+                    const bool second = kb >= g.kb0;
+                    const int k = (second ? kb - g.kb0 : kb) * kBK;
+                    if constexpr (EPI == EPI_LINEAR) {
+                        const CUtensorMap* ma = second ? &a1 : &a0;
+                        if (g.a_mn) {
+                            tma_2d<1>(sa, ma, tn * 128, k, bar);
+                            tma_2d<1>(sa + kABytes / 2, ma, tn * 128 + 64, k, bar);
+                        } else {
+                            tma_2d<1>(sa, ma, k, tn * 128, bar);
+                        }
+                    } else {
+                        for (int q = 0; q < 4; ++q) {
+                            tma_2d<1>(sa + q * 4096, &a0, k, tn * 64 + q * 16, bar);
+                            tma_2d<1>(sa + q * 4096 + 2048, &a1, k, tn * 64 + q * 16, bar);
+                        }
+                    }
+                    const CUtensorMap* mb = second ? &b1 : &b0;
+                    if (g.b_mn) {
+                        for (int j = 0; j < g.bn / 64; ++j)
+                            tma_2d<1>(sb + j * 8192, mb, tt * g.bn + j * 64, k, bar);
+                    } else {
+                        tma_2d<1>(sb, mb, k, tt * g.bn, bar);
+                    }
+                }
+            }
+            if (!ok)  // let the copies in flight land before the CTA ends
+                for (int i = it > g.stages ? it - g.stages : 0; i < it; ++i)
+                    mbar_drain(full + 8 * (i % g.stages), (i / g.stages) & 1);
+        }
+        __syncwarp();
+    } else if (warp == 9) {  // --------------------------------------- issuer
+        if (lane == 0) {
+            const uint32_t a_lbo = g.a_mn ? 8192 : 16, b_lbo = g.b_mn ? 8192 : 16;
+            const uint64_t a_step = g.a_mn ? 2048 >> 4 : 32 >> 4, b_step = g.b_mn ? 2048 >> 4 : 32 >> 4;
+            int it = 0, local = 0;
+            bool ok = true;
+            for (int tile = first; tile < tiles && ok; tile += step, ++local) {
+                const int buf = local & 1;
+                if (!(ok = mbar_wait(tempty + 8 * buf, ((local >> 1) & 1) ^ 1, dead))) break;
+                tc_fence_after();
+                const uint32_t d = tmem + buf * g.bn;
+                for (int kb = k_lo; kb < k_hi; ++kb, ++it) {
+                    const int st = it % g.stages, ph = (it / g.stages) & 1;
+                    if (!(ok = mbar_wait(full + 8 * st, ph, dead))) break;
+                    tc_fence_after();
+                    const uint32_t sa = ring + st * sbytes, sb = sa + kABytes;
+                    const uint64_t da = make_desc(sa, a_lbo, 1024), db = make_desc(sb, b_lbo, 1024);
+#pragma unroll
+                    for (int ks = 0; ks < kBK / 16; ++ks)
+                        mma_ss<1>(d, da + ks * a_step, db + ks * b_step, g.idesc, kb > k_lo || ks > 0);
+                    tc_commit(empty + 8 * st);
+                }
+                if (ok) tc_commit(tfull + 8 * buf);
+            }
+            if (!ok) {
+                tc_commit(drain);
+                mbar_drain(drain, 0);
+            }
+        }
+        __syncwarp();
+    } else {  // ------------------------------------------------------ epilogue
+        const int quad = warp & 3, half = warp >> 2;
+        int local = 0;
+        for (int tile = first; tile < tiles; tile += step, ++local) {
+            const int buf = local & 1;
+            int tn, tt;
+            place(tile, tn, tt);
+            float bias = 0.f;
+            if constexpr (EPI == EPI_LINEAR) {
+                const int64_t n = (int64_t)tn * 128 + quad * 32 + lane;
+                if (g.bias && n < g.N) bias = to_f<T>(((const T*)g.bias)[n]);
+            }
+            if (!__all_sync(0xffffffffu, mbar_wait(tfull + 8 * buf, (local >> 1) & 1, dead))) break;
+            tc_fence_after();
+            const uint32_t src = tmem + buf * g.bn + ((uint32_t)(quad * 32) << 16);
+            const int64_t t0 = (int64_t)tt * g.bn;
+            const int valid = (int)min((int64_t)g.bn, g.M - t0);
+            if (g.splits > 1) {  // the partial tile, [token][feature], for the cluster to sum
+                float* part = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)));
+                for (int c = half * 16; c < valid; c += 32) {
+                    uint32_t r[16];
+                    tmem_ld16(src + c, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) part[(c + j) * 128 + quad * 32 + lane] = __uint_as_float(r[j]);
+                }
+            } else {
+                for (int c = half * 32; c < valid; c += 64) {
+                    if (g.bn >= 32) {
+                        uint32_t r[32];
+                        tmem_ld32(src + c, r);
+                        tmem_wait_ld();
+                        emit_act<EPI, 32, T, O>(g, reinterpret_cast<const float*>(r), tn, quad, lane, t0 + c, bias);
+                    } else {
+                        uint32_t r[16];
+                        tmem_ld16(src + c, r);
+                        tmem_wait_ld();
+                        emit_act<EPI, 16, T, O>(g, reinterpret_cast<const float*>(r), tn, quad, lane, t0 + c, bias);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tempty + 8 * buf);
+        }
+    }
+
+    if (g.splits > 1) {
+        __syncwarp();
+        cluster_sync_all();
+        if (warp < 8 && !*dead) {
+            int tn, tt;
+            place(first, tn, tt);
+            const int64_t t0 = (int64_t)tt * g.bn;
+            const int valid = (int)min((int64_t)g.bn, g.M - t0);
+            const int pairs = (valid + 1) / 2;
+            for (int u = rank * 8 + warp; u < 4 * pairs; u += 8 * g.splits) {
+                const int quad = u & 3, c = (u >> 2) * 2;
+                float v[2] = {0.f, 0.f};
+                const uint32_t at = ring + (uint32_t)(c * 128 + quad * 32 + lane) * 4;
+                for (int s = 0; s < g.splits; ++s) {
+                    const uint32_t ra = map_rank(at, s);
+                    v[0] += ld_cluster_f32(ra);
+                    v[1] += ld_cluster_f32(ra + 512);
+                }
+                float bias = 0.f;
+                if constexpr (EPI == EPI_LINEAR) {
+                    const int64_t n = (int64_t)tn * 128 + quad * 32 + lane;
+                    if (g.bias && n < g.N) bias = to_f<T>(((const T*)g.bias)[n]);
+                }
+                emit_act<EPI, 2, T, O>(g, v, tn, quad, lane, t0 + c, bias);
+            }
+        }
+        __syncwarp();
+        cluster_sync_all();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9) tmem_free<1>(tmem, cols);
+}
+
+// ------------------------------------------------------------------ launch
+struct Operand {
+    const void* p;
+    int64_t ld;  // elements between rows
+    bool mn;     // rows run over k (the M or N index is the contiguous one)
+};
+
+// Tile width (tokens) and split of the reduction, by an estimate of the time in SM clocks: a
+// k-block costs what its product takes (16 columns x 128 rows x 64 deep in 16 clocks) or what
+// its bytes take at an SM's share of HBM (24 bytes a clock), whichever is more; a tile costs
+// its start and end besides, and a split the exchange through shared memory.
+struct Plan {
+    int bn, splits, grid;
+};
+
+Plan make_plan(int64_t n_tiles, int64_t M, int kb, int sms, int min_bn, int per_tile_bytes) {
+    Plan best{};
+    double best_cost = 1e300;
+    for (int bn = min_bn; bn <= 256; bn *= 2) {
+        const int64_t tt = (M + bn - 1) / bn, tiles = n_tiles * tt;
+        for (int s = 1; s <= 8; s *= 2) {
+            if (s > 1 && (s > kb || tiles * s > sms)) break;
+            const double per_kb = fmax(bn, (kABytes + bn * 128.0) / 24.0);
+            const double waves = s > 1 ? 1.0 : (double)((tiles + sms - 1) / sms);
+            const double body = (double)((kb + s - 1) / s) * per_kb;
+            const double tail = 600.0 + per_tile_bytes * bn * 4.0 + (s > 1 ? 1200.0 + 128.0 * 4.0 * bn / 16.0 : 0.0);
+            const double cost = waves * fmax(body, s > 1 ? 0.0 : tail) + tail + 1500.0;
+            if (cost < best_cost) {
+                best_cost = cost;
+                best.bn = bn;
+                best.splits = s;
+                best.grid = (int)(s > 1 ? tiles * s : (tiles < sms ? tiles : sms));
+            }
+        }
+        if (bn >= M) break;
+    }
+    return best;
+}
+
+template <int EPI, typename T, typename O>
+int launch(const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0, const CUtensorMap& b1, const GemmArgs& g,
+           int grid, cudaStream_t stream) {
+    const int smem = g.stages * (kABytes + g.bn * kBK * 2) + 1024;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    static std::atomic<bool> ready[64];
+    if (dev >= 64 || !ready[dev].load()) {
+        cudaError_t e = cudaFuncSetAttribute(gemm_kernel<EPI, T, O>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kRingBytes + 1024);
+        if (e != cudaSuccess) return op_fail(KD_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+        if (dev < 64) ready[dev].store(true);
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kGemmThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    if (g.splits > 1) {
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = g.splits;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+    }
+    cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_kernel<EPI, T, O>, a0, a1, b0, b1, g);
+    if (e != cudaSuccess) return op_fail(KD_ECUDA, "launch failed: %s", cudaGetErrorString(e));
+    return KD_OK;
+}
+
+int operand_map(CUtensorMap* m, int dtype, const Operand& o, int64_t rows, int64_t k, int box_rows) {
+    if (o.mn) return make_map_2d(m, dtype, o.p, rows, k, o.ld, 64, kBK);
+    return make_map_2d(m, dtype, o.p, k, rows, o.ld, kBK, box_rows);
+}
+
+template <int EPI, typename T, typename O>
+int run_typed(GemmArgs g, int dtype, const Operand* a, const Operand* b, int pairs, int64_t k, cudaStream_t stream) {
+    int sms = 0;
+    int rc = op_sm_count(&sms);
+    if (rc) return rc;
+    const bool gated = EPI != EPI_LINEAR;
+    const int per = gated ? 64 : 128;
+    const int64_t n_tiles = (g.N + per - 1) / per;
+    const int64_t kblocks = (k + kBK - 1) / kBK;
+    g.kb0 = (int)kblocks;
+    g.kb = (int)(kblocks * (gated ? 1 : pairs));
+    const Plan p = make_plan(n_tiles, g.M, g.kb, sms, b[0].mn ? 64 : 16, (int)sizeof(O));
+    const int64_t t_tiles = (g.M + p.bn - 1) / p.bn;
+    if (n_tiles * t_tiles > 0x3fffffff) return op_fail(KD_EINVAL, "too many output tiles");
+    g.n_tiles = (int)n_tiles;
+    g.t_tiles = (int)t_tiles;
+    g.bn = p.bn;
+    g.splits = p.splits;
+    g.a_mn = a[0].mn;
+    g.b_mn = b[0].mn;
+    g.stages = kRingBytes / (kABytes + p.bn * kBK * 2);
+    if (g.stages > kMaxRing) g.stages = kMaxRing;
+    g.idesc = make_idesc(128, p.bn, dtype == KD_BF16, g.a_mn, g.b_mn);
+    CUtensorMap ma[2], mb[2];
+    const int a_box = gated ? 16 : 128;
+    if ((rc = operand_map(&ma[0], dtype, a[0], g.N, k, a_box))) return rc;
+    if ((rc = operand_map(&mb[0], dtype, b[0], g.M, k, p.bn))) return rc;
+    ma[1] = ma[0];
+    mb[1] = mb[0];
+    if (pairs > 1) {
+        if ((rc = operand_map(&ma[1], dtype, a[1], g.N, k, a_box))) return rc;
+        if (!gated && (rc = operand_map(&mb[1], dtype, b[1], g.M, k, p.bn))) return rc;
+    }
+    return launch<EPI, T, O>(ma[0], ma[1], mb[0], mb[1], g, p.grid, stream);
+}
+
+template <int EPI>
+int run(const GemmArgs& g, int dtype, int out_dtype, const Operand* a, const Operand* b, int pairs, int64_t k,
+        cudaStream_t s) {
+    if constexpr (EPI == EPI_LINEAR) {
+        if (out_dtype == KD_F32)
+            return dtype == KD_BF16 ? run_typed<EPI, __nv_bfloat16, float>(g, dtype, a, b, pairs, k, s)
+                                    : run_typed<EPI, __half, float>(g, dtype, a, b, pairs, k, s);
+    }
+    return dtype == KD_BF16 ? run_typed<EPI, __nv_bfloat16, __nv_bfloat16>(g, dtype, a, b, pairs, k, s)
+                            : run_typed<EPI, __half, __half>(g, dtype, a, b, pairs, k, s);
+}
+
+bool known_act(int a) { return a >= KD_ACT_NONE && a <= KD_ACT_GELU; }
+
+// A 16-bit matrix that TMA reads: 16-byte aligned base, and rows that start on 16 bytes.
+int check_operand(const char* what, const void* p, int64_t rows, int64_t cols, int64_t* ld) {
+    if (!p) return op_fail(KD_EINVAL, "%s: NULL pointer", what);
+    if ((uintptr_t)p & 15) return op_fail(KD_EINVAL, "%s: not 16-byte aligned", what);
+    if (rows == 1) {  // the distance of rows is not used
+        *ld = (cols + 7) & ~(int64_t)7;
+        return KD_OK;
+    }
+    if (*ld < cols || *ld % 8 || *ld >= (int64_t)1 << 38)
+        return op_fail(KD_EINVAL, "%s: rows of %lld elements, %lld apart (need a multiple of 8, at least the row)", what,
+                       (long long)cols, (long long)*ld);
+    return KD_OK;
+}
+
+int check_rows(const char* what, const void* p, int elem, int64_t rows, int64_t cols, int64_t ld) {
+    if (!p) return op_fail(KD_EINVAL, "%s: NULL pointer", what);
+    if ((uintptr_t)p % elem) return op_fail(KD_EINVAL, "%s: misaligned pointer", what);
+    if (rows > 1 && ld < cols) return op_fail(KD_EINVAL, "%s: rows of %lld elements, %lld apart", what, (long long)cols, (long long)ld);
+    return KD_OK;
+}
+
+constexpr int64_t kMaxDim = 0x7fffffff - 1024;  // TMA coordinates are 32-bit
+
+int check_sizes(const char* who, int dtype, int act, int64_t m, int64_t n, int64_t k) {
+    if (dtype != KD_BF16 && dtype != KD_F16) return op_fail(KD_EINVAL, "%s: dtype must be KD_BF16 or KD_F16", who);
+    if (!known_act(act)) return op_fail(KD_EINVAL, "%s: unknown activation %d", who, act);
+    if (m < 0 || n < 0 || k < 1 || m > kMaxDim || n > kMaxDim || k > kMaxDim)
+        return op_fail(KD_EINVAL, "%s: sizes m=%lld n=%lld k=%lld out of range", who, (long long)m, (long long)n, (long long)k);
+    return KD_OK;
+}
+
+}  // namespace
+
+int gemm_status(cudaStream_t s, unsigned int* st) {
+    cudaError_t e = cudaMemcpyFromSymbolAsync(st, g_op_status, sizeof *st, 0, cudaMemcpyDeviceToHost, s);
+    const unsigned int zero = 0;
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e == cudaSuccess && *st) {
+        e = cudaMemcpyToSymbolAsync(g_op_status, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, s);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    }
+    return e == cudaSuccess ? KD_OK : op_fail(KD_ECUDA, "kd_op_sync: %s", cudaGetErrorString(e));
+}
+
+}  // namespace kd
+
+using namespace kd;
+
+extern "C" {
+
+const char* kd_op_error(void) { return t_err; }
+
+int kd_op_sync(void* stream) {
+    unsigned int a = 0;
+    int rc = gemm_status((cudaStream_t)stream, &a);
+    if (rc) return rc;
+    if (a) return op_fail(KD_ETIMEOUT, "a device-side wait of an operator exceeded its limit");
+    return KD_OK;
+}
+
+int kd_linear(const kd_linear_args* p, void* stream) {
+    if (!p) return op_fail(KD_EINVAL, "kd_linear: NULL arguments");
+    kd_linear_args q = *p;
+    int rc = check_sizes("kd_linear", q.dtype, q.act, q.m, q.n, q.k);
+    if (rc) return rc;
+    if (q.out_dtype != q.dtype && q.out_dtype != KD_F32)
+        return op_fail(KD_EINVAL, "kd_linear: out_dtype must be the input type or KD_F32");
+    if (q.w_transposed != 0 && q.w_transposed != 1) return op_fail(KD_EINVAL, "kd_linear: w_transposed must be 0 or 1");
+    if (q.m == 0 || q.n == 0) return KD_OK;
+    const int oe = q.out_dtype == KD_F32 ? 4 : 2;
+    if ((rc = check_operand("kd_linear: x", q.x, q.m, q.k, &q.ld_x))) return rc;
+    if ((rc = check_operand("kd_linear: w", q.w, q.w_transposed ? q.k : q.n, q.w_transposed ? q.n : q.k, &q.ld_w))) return rc;
+    if (q.bias && (uintptr_t)q.bias % 2) return op_fail(KD_EINVAL, "kd_linear: bias: misaligned pointer");
+    if (q.residual && (rc = check_rows("kd_linear: residual", q.residual, oe, q.m, q.n, q.ld_residual))) return rc;
+    if ((rc = check_rows("kd_linear: out", q.out, oe, q.m, q.n, q.ld_out))) return rc;
+    GemmArgs g{};
+    g.N = q.n, g.M = q.m, g.act = q.act;
+    g.bias = q.bias, g.res = q.residual, g.ld_res = q.ld_residual, g.out = q.out, g.ld_out = q.ld_out;
+    const Operand a{q.w, q.ld_w, q.w_transposed != 0}, b{q.x, q.ld_x, false};
+    return run<EPI_LINEAR>(g, q.dtype, q.out_dtype, &a, &b, 1, q.k, (cudaStream_t)stream);
+}
+
+static int check_gated(const char* who, kd_gated_args* q) {
+    int rc = check_sizes(who, q->dtype, q->act, q->m, q->f, q->d);
+    if (rc) return rc;
+    if (q->m == 0 || q->f == 0) return KD_OK;
+    if ((rc = check_operand("gated block: x", q->x, q->m, q->d, &q->ld_x))) return rc;
+    if ((rc = check_operand("gated block: wg", q->wg, q->f, q->d, &q->ld_wg))) return rc;
+    return check_operand("gated block: wu", q->wu, q->f, q->d, &q->ld_wu);
+}
+
+int kd_gated_ffn(const kd_gated_args* p, void* h, int64_t ld_h, void* stream) {
+    if (!p) return op_fail(KD_EINVAL, "kd_gated_ffn: NULL arguments");
+    kd_gated_args q = *p;
+    int rc = check_gated("kd_gated_ffn", &q);
+    if (rc || q.m == 0 || q.f == 0) return rc;
+    if ((rc = check_rows("kd_gated_ffn: h", h, 2, q.m, q.f, ld_h))) return rc;
+    GemmArgs g{};
+    g.N = q.f, g.M = q.m, g.act = q.act, g.out = h, g.ld_out = ld_h;
+    const Operand a[2] = {{q.wg, q.ld_wg, false}, {q.wu, q.ld_wu, false}}, b{q.x, q.ld_x, false};
+    return run<EPI_GATED>(g, q.dtype, q.dtype, a, &b, 2, q.d, (cudaStream_t)stream);
+}
+
+static int64_t gated_ld(int64_t f) { return (f + 63) & ~(int64_t)63; }
+
+size_t kd_gated_ffn_backward_workspace(int64_t m, int64_t f) {
+    if (m < 0 || f < 0 || m > kMaxDim || f > kMaxDim) return 0;
+    return (size_t)m * gated_ld(f) * 2 * 2 + 256;
+}
+
+int kd_gated_ffn_backward(const kd_gated_args* p, const void* dh, int64_t ld_dh, void* dx, int64_t ld_dx, void* dwg,
+                          int64_t ld_dwg, void* dwu, int64_t ld_dwu, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+    if (!p) return op_fail(KD_EINVAL, "kd_gated_ffn_backward: NULL arguments");
+    kd_gated_args q = *p;
+    int rc = check_gated("kd_gated_ffn_backward", &q);
+    if (rc) return rc;
+    if (q.m == 0 || q.f == 0) return op_fail(KD_EINVAL, "kd_gated_ffn_backward: m and f must be at least 1");
+    if ((rc = check_rows("kd_gated_ffn_backward: dh", dh, 2, q.m, q.f, ld_dh))) return rc;
+    if (dx && (rc = check_rows("kd_gated_ffn_backward: dx", dx, 2, q.m, q.d, ld_dx))) return rc;
+    if (dwg && (rc = check_rows("kd_gated_ffn_backward: dwg", dwg, 2, q.f, q.d, ld_dwg))) return rc;
+    if (dwu && (rc = check_rows("kd_gated_ffn_backward: dwu", dwu, 2, q.f, q.d, ld_dwu))) return rc;
+    if (!workspace || workspace_bytes < kd_gated_ffn_backward_workspace(q.m, q.f))
+        return op_fail(KD_ENOMEM, "kd_gated_ffn_backward: workspace of %zu bytes, need %zu", workspace_bytes,
+                       kd_gated_ffn_backward_workspace(q.m, q.f));
+    const int64_t ld = gated_ld(q.f);
+    uint8_t* base = (uint8_t*)(((uintptr_t)workspace + 255) & ~(uintptr_t)255);
+    uint8_t* dg = base;
+    uint8_t* du = base + (size_t)q.m * ld * 2;
+    cudaStream_t s = (cudaStream_t)stream;
+    // dg = dh u act'(g), du = dh act(g), with g and u recomputed. They are rounded to the input
+    // type once: the next two products take 16-bit operands, and one more rounding of the terms
+    // of a sum is of the size of the rounding of its result.
+    {
+        GemmArgs g{};
+        g.N = q.f, g.M = q.m, g.act = q.act, g.res = dh, g.ld_res = ld_dh, g.out = dg, g.out2 = du, g.ld_out = ld;
+        const Operand a[2] = {{q.wg, q.ld_wg, false}, {q.wu, q.ld_wu, false}}, b{q.x, q.ld_x, false};
+        if ((rc = run<EPI_GATED_BWD>(g, q.dtype, q.dtype, a, &b, 2, q.d, s))) return rc;
+    }
+    if (dx) {  // dx[t][c] = sum_f dg[t][f] wg[f][c] + du[t][f] wu[f][c]: one sum over both pairs
+        GemmArgs g{};
+        g.N = q.d, g.M = q.m, g.out = dx, g.ld_out = ld_dx;
+        const Operand a[2] = {{q.wg, q.ld_wg, true}, {q.wu, q.ld_wu, true}}, b[2] = {{dg, ld, false}, {du, ld, false}};
+        if ((rc = run<EPI_LINEAR>(g, q.dtype, q.dtype, a, b, 2, q.f, s))) return rc;
+    }
+    for (int i = 0; i < 2; ++i) {  // dwg[f][c] = sum_t dg[t][f] x[t][c]
+        void* dw = i ? dwu : dwg;
+        if (!dw) continue;
+        GemmArgs g{};
+        g.N = q.d, g.M = q.f, g.out = dw, g.ld_out = i ? ld_dwu : ld_dwg;
+        const Operand a{q.x, q.ld_x, true}, b{i ? du : dg, ld, true};
+        if ((rc = run<EPI_LINEAR>(g, q.dtype, q.dtype, &a, &b, 1, q.m, s))) return rc;
+    }
+    return KD_OK;
+}
+
+}  // extern "C"
