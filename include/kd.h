@@ -270,6 +270,29 @@ int kd_gated_ffn_backward(const kd_gated_args *args, const void *dh, int64_t ld_
                           int64_t ld_dwg, void *dwu, int64_t ld_dwu, void *workspace, size_t workspace_bytes,
                           void *stream);
 
+/* Attention of n new tokens of one request over its key-value cache: token i of q sees the
+ * positions 0 .. kv_len + i of k and v, which hold the kv_len earlier ones and the n new ones.
+ * q [n][n_heads][head_dim], out the same; k and v [n_kv_heads][>= kv_len + n][head_dim] (the
+ * layout of kd_kv_ptr); query head h reads kv head h * n_kv_heads / n_heads. head_dim is 64 or
+ * 128; strides count elements, are multiples of 8 and may be in any order (positions before
+ * heads too); all four start on 16 bytes. scale is usually 1 / sqrt(head_dim). One token or a
+ * long prompt; n may be 0. Cache rows at and after kv_len + n are never used. A position that a
+ * token does not see has weight 0 in its sum, so v has to be finite at all kv_len + n. */
+typedef struct kd_attention_args {
+    int32_t dtype, n_heads, n_kv_heads, head_dim;
+    int64_t n, kv_len;
+    const void *q;
+    int64_t q_token, q_head;
+    const void *k;
+    int64_t k_pos, k_head;
+    const void *v;
+    int64_t v_pos, v_head;
+    void *out;
+    int64_t out_token, out_head;
+    float scale;
+} kd_attention_args;
+int kd_prompt_attention(const kd_attention_args *args, void *stream);
+
 /* Wait for `stream` and report a device-side wait of an operator that ran out of its limit
  * (2 s; such a kernel ends early and its outputs are not valid): KD_OK or KD_ETIMEOUT, once. */
 int kd_op_sync(void *stream);

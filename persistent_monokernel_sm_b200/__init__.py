@@ -17,10 +17,10 @@ __all__ = ["KdError", "kd_config", "kd_weights", "kd_info", "load_library", "Dec
            "kd_decode", "kd_generate", "kd_sync", "kd_position", "kd_set_trace", "kd_set_timeout", "kd_set_sampling", "kd_decode_noalloc", "kd_get_info", "kd_kv_ptr",
            "kd_last_error", "kd_strerror", "kd_destroy", "LIB_PATH", "ERRORS",
            "kd_linear_args", "kd_gated_args", "kd_linear", "kd_gated_ffn", "kd_gated_ffn_backward_workspace",
-           "kd_gated_ffn_backward", "kd_op_sync", "kd_op_error",
-           "linear", "gated_ffn", "gated_ffn_backward"]
+           "kd_gated_ffn_backward", "kd_attention_args", "kd_prompt_attention", "kd_op_sync", "kd_op_error",
+           "linear", "gated_ffn", "gated_ffn_backward", "prompt_attention"]
 
-_OPERATORS = ("linear", "gated_ffn", "gated_ffn_backward")
+_OPERATORS = ("linear", "gated_ffn", "gated_ffn_backward", "prompt_attention")
 
 
 def __getattr__(name):
@@ -76,6 +76,16 @@ class kd_gated_args(ctypes.Structure):
                 ("wu", ctypes.c_void_p), ("ld_wu", ctypes.c_int64)]
 
 
+class kd_attention_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "n_heads", "n_kv_heads", "head_dim")] + \
+               [(n, ctypes.c_int64) for n in ("n", "kv_len")] + \
+               [("q", ctypes.c_void_p), ("q_token", ctypes.c_int64), ("q_head", ctypes.c_int64),
+                ("k", ctypes.c_void_p), ("k_pos", ctypes.c_int64), ("k_head", ctypes.c_int64),
+                ("v", ctypes.c_void_p), ("v_pos", ctypes.c_int64), ("v_head", ctypes.c_int64),
+                ("out", ctypes.c_void_p), ("out_token", ctypes.c_int64), ("out_head", ctypes.c_int64),
+                ("scale", ctypes.c_float)]
+
+
 class KdError(RuntimeError):
     def __init__(self, code, msg=""):
         super().__init__("%s (%d): %s" % (ERRORS.get(code, "?"), code, msg))
@@ -121,6 +131,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "kd_gated_ffn": (ctypes.c_int, [ctypes.c_char_p, _P, ctypes.c_int64, _P]),
         "kd_gated_ffn_backward_workspace": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64]),
         "kd_gated_ffn_backward": (ctypes.c_int, [ctypes.c_char_p] + [_P, ctypes.c_int64] * 4 + [_P, ctypes.c_size_t, _P]),
+        "kd_prompt_attention": (ctypes.c_int, [ctypes.c_char_p, _P]),
         "kd_op_sync": (ctypes.c_int, [_P]),
         "kd_op_error": (ctypes.c_char_p, []),
     }
@@ -251,6 +262,10 @@ def kd_gated_ffn_backward(args: kd_gated_args, dh: int, ld_dh: int, dx: int | No
                           stream: int | None) -> int:
     return _check_op(load_library().kd_gated_ffn_backward(bytes(args), dh, ld_dh, dx, ld_dx, dwg, ld_dwg, dwu, ld_dwu,
                                                           workspace, workspace_bytes, stream), "kd_gated_ffn_backward")
+
+
+def kd_prompt_attention(args: kd_attention_args, stream: int | None) -> int:
+    return _check_op(load_library().kd_prompt_attention(bytes(args), stream), "kd_prompt_attention")
 
 
 def kd_op_sync(stream: int | None) -> int:

@@ -1,0 +1,502 @@
+// kd_attention.cu -- causal attention of n new tokens over a key-value cache that holds kv_len
+// earlier positions and the new ones, on the 5th-generation tensor cores.
+//
+// o_i = sum_j p_ij v_j, p_i = softmax_j(scale q_i . k_j) over the positions j <= kv_len + i; in
+// one pass over j with a running maximum m, sum l and unnormalised output o (online softmax).
+//
+// Rows: the r query heads of a kv head share its keys and values, so a tile's 128 rows are
+// 128 / r tokens x r heads: keys and values are read once per kv head, and one token of a
+// grouped model is one tile. A thread owns a row: no reduction crosses threads.
+//
+// A CTA has two streams, each a warpgroup with its own scores (128 x 128 fp32) and output
+// (128 x hd fp32) in tensor memory; while one does its softmax the tensor cores work for the
+// other. For prompts the streams are two neighbouring tiles that share every key and value
+// block. With few tiles they share one tile and take alternate blocks, and the blocks are
+// split over the CTAs of a cluster besides; the partial (m, l, o) are then joined through
+// (distributed) shared memory in a fixed order.
+//
+// Per block and stream: S = Q K^T; p = 2^(s - m) in 16 bits written over S; O += P V with P
+// read from tensor memory. A row's reference m is raised (and O rescaled) only when its maximum
+// has grown by more than 2^8: p then stays within 2^8 and O within range of fp32.
+// p is rounded to 16 bits as an operand of the second product (off by half a step of its type,
+// averaged over the row); its sum l is taken in fp32 before that rounding.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+
+#include "kd.h"
+#include "kd_ops.h"
+#include "kd_sm100.h"
+
+namespace kd {
+namespace {
+
+constexpr int kThr = 320;   // two warpgroups of softmax, the producer's warp, the issuer's warp
+constexpr int kKeys = 128;  // positions per block
+constexpr float kLazy = 8.f;
+
+struct AttnArgs {
+    int n, kv_len, r, hkv;
+    int tq;      // tokens per tile
+    int tiles;   // query tiles
+    int splits;  // CTAs per cluster
+    int shared;  // the streams share a tile (alternate blocks)
+    uint32_t idesc_s, idesc_o;
+    float scale_log2;
+    void* out;
+    int64_t out_token, out_head;
+};
+
+template <int HD> struct Shape {
+    static constexpr int block = kKeys * HD * 2;           // bytes of a key, value or query tile
+    static constexpr int slots = HD == 128 ? 5 : 8;        // of the ring of key and value blocks
+    static constexpr int part = HD + 4;                    // floats between rows of a partial output
+    static constexpr int smem = 1024 + (2 + slots) * block;
+    static_assert(2 * 128 * part * 4 <= slots * block, "the partial outputs fit the ring");
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15};" ::KD_I8(r, 0),
+        KD_I8(r, 8), "r"(addr)
+        : "memory");
+}
+
+template <int HD, typename T>
+__global__ void __launch_bounds__(kThr, 1)
+    attention_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                     const __grid_constant__ CUtensorMap mv, const __grid_constant__ AttnArgs a) {
+    constexpr int kSlots = Shape<HD>::slots, kBlock = Shape<HD>::block, kPart = Shape<HD>::part, kHalves = HD / 64;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t s_full[kSlots], s_empty[kSlots], s_q, s_s[2], s_p[2], s_o[2], s_drain;
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int s_dead;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t qs = (smem_u32(smem_raw) + 1023) & ~1023u;
+    const uint32_t ring = qs + 2 * kBlock;
+    const uint32_t full = smem_u32(s_full), empty = smem_u32(s_empty), qbar = smem_u32(&s_q);
+    const uint32_t sbar = smem_u32(s_s), pbar = smem_u32(s_p), obar = smem_u32(s_o), drain = smem_u32(&s_drain);
+    volatile int* dead = &s_dead;
+    // (m, l) of the two streams' rows for the join: where a second query tile would be
+    float* stat = reinterpret_cast<float*>(smem_raw + (qs + kBlock - smem_u32(smem_raw)));
+    const uint32_t stat_at = qs + kBlock;
+
+    // What this CTA works on: a kv head, one or two tiles, a range of blocks per stream.
+    const int rank = a.splits > 1 ? (int)cluster_rank() : 0;
+    const int unit = blockIdx.x / a.splits;
+    const int g = unit % a.hkv;
+    int tile[2], nb[2], lo = 0, total;  // nb: blocks of each stream; total: blocks streamed
+    auto blocks_of = [&](int t) {
+        const int last = min(a.n, (t + 1) * a.tq);  // one past its last token
+        return (a.kv_len + last + kKeys - 1) / kKeys;
+    };
+    if (a.shared) {
+        tile[0] = tile[1] = a.tiles - 1 - unit / a.hkv;
+        const int all = blocks_of(tile[0]);
+        lo = (int)((long long)all * rank / a.splits);
+        total = (int)((long long)all * (rank + 1) / a.splits) - lo;
+        nb[0] = (total + 1) / 2, nb[1] = total / 2;
+    } else {  // the longest rows first
+        const int pair = (a.tiles + 1) / 2 - 1 - unit / a.hkv;
+        tile[0] = 2 * pair, tile[1] = 2 * pair + 1;
+        nb[0] = blocks_of(tile[0]);
+        nb[1] = tile[1] < a.tiles ? blocks_of(tile[1]) : 0;
+        total = max(nb[0], nb[1]);
+    }
+    // Order of the ring: K_0 (and K_1 with alternate blocks), then V_i, K_(i + ahead) in turn.
+    const int ahead = min(a.shared ? 2 : 1, total);
+    auto seq_k = [&](int i) { return i < ahead ? i : ahead + 2 * (i - ahead) + 1; };
+    auto seq_v = [&](int i) { return ahead + i + min(i, total - ahead); };
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kSlots; ++i) mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, 1);
+        mbar_init(qbar, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(sbar + 8 * i, 1), mbar_init(pbar + 8 * i, 4), mbar_init(obar + 8 * i, 1);
+        mbar_init(drain, 1);
+        s_dead = 0;
+        fence_barrier_init();
+    }
+    if (warp == 8 && lane == 0) {
+        tma_prefetch(&mq);
+        tma_prefetch(&mk);
+        tma_prefetch(&mv);
+    }
+    if (warp == 9) tmem_alloc<1>(smem_u32(&s_tmem), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;  // columns: S0, S1 (128 each), O0, O1 (HD each)
+
+    if (warp == 8) {  // ---------------------------------------------- producer
+        if (lane == 0) {
+            const int two = !a.shared && tile[1] < a.tiles ? 2 : 1;
+            mbar_expect(qbar, two * kHalves * a.tq * a.r * 128);
+            for (int s = 0; s < two; ++s)
+                for (int h = 0; h < kHalves; ++h)
+                    tma_3d(qs + s * kBlock + h * 16384, &mq, h * 64, g * a.r, tile[s] * a.tq, qbar);
+            int it = 0;
+            bool ok = true;
+            auto load = [&](const CUtensorMap* m, int block) {
+                const int st = it % kSlots;
+                if (!ok || !(ok = mbar_wait(empty + 8 * st, ((it / kSlots) & 1) ^ 1, dead))) return;
+                mbar_expect(full + 8 * st, kBlock);
+                for (int h = 0; h < kHalves; ++h)
+                    tma_3d(ring + st * kBlock + h * 16384, m, h * 64, (lo + block) * kKeys, g, full + 8 * st);
+                ++it;
+            };
+            for (int i = 0; i < ahead; ++i) load(&mk, i);
+            for (int i = 0; i < total && ok; ++i) {
+                load(&mv, i);
+                if (i + ahead < total) load(&mk, i + ahead);
+            }
+            if (!ok) {  // let the copies in flight land before the CTA ends
+                mbar_drain(qbar, 0);
+                for (int i = it > kSlots ? it - kSlots : 0; i < it; ++i)
+                    mbar_drain(full + 8 * (i % kSlots), (i / kSlots) & 1);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 9) {  // --------------------------------------- issuer
+        if (lane == 0) {
+            bool ok = mbar_wait(qbar, 0, dead);
+            auto wait_seq = [&](int q) { return ok = ok && mbar_wait(full + 8 * (q % kSlots), (q / kSlots) & 1, dead); };
+            auto free_seq = [&](int q) { tc_commit(empty + 8 * (q % kSlots)); };
+            auto scores = [&](int s, int q) {  // S_s = Q K^T from slot q
+                const uint32_t ka = ring + (q % kSlots) * kBlock, qa = qs + (a.shared ? 0 : s) * kBlock;
+#pragma unroll
+                for (int ks = 0; ks < HD / 16; ++ks) {
+                    const uint32_t off = (ks >> 2) * 16384 + (ks & 3) * 32;
+                    mma_ss<1>(tmem + s * 128, make_desc(qa + off, 16, 1024), make_desc(ka + off, 16, 1024), a.idesc_s, ks > 0);
+                }
+                tc_commit(sbar + 8 * s);
+            };
+            auto values = [&](int s, int i, int q) {  // O_s += P_s V from slot q; i: block of the stream
+                if (!(ok = ok && mbar_wait(pbar + 8 * s, i & 1, dead))) return;
+                tc_fence_after();
+                const uint32_t va = ring + (q % kSlots) * kBlock;
+#pragma unroll
+                for (int ks = 0; ks < kKeys / 16; ++ks)
+                    mma_ts(tmem + 256 + s * HD, tmem + s * 128 + ks * 8, make_desc(va + ks * 2048, 16384, 1024), a.idesc_o,
+                           i > 0 || ks > 0);
+                if (i == nb[s] - 1) tc_commit(obar + 8 * s);
+            };
+            tc_fence_after();
+            if (a.shared) {
+                for (int i = 0; i < ahead && wait_seq(i); ++i) {
+                    tc_fence_after();
+                    scores(i, i);
+                    free_seq(i);
+                }
+                for (int i = 0; i < total && ok; ++i) {
+                    const int s = i & 1, v = seq_v(i);
+                    if (!wait_seq(v)) break;
+                    values(s, i >> 1, v);
+                    if (!ok) break;
+                    free_seq(v);
+                    if (i + 2 < total) {
+                        const int k = seq_k(i + 2);
+                        if (!wait_seq(k)) break;
+                        tc_fence_after();
+                        scores(s, k);
+                        free_seq(k);
+                    }
+                }
+            } else if (wait_seq(0)) {
+                tc_fence_after();
+                scores(0, 0);
+                if (nb[1] > 0) scores(1, 0);
+                free_seq(0);
+                for (int i = 0; i < total && ok; ++i) {
+                    const int v = seq_v(i), k = i + 1 < total ? seq_k(i + 1) : -1;
+                    if (!wait_seq(v)) break;
+                    for (int s = 0; s < 2 && ok; ++s) {
+                        if (i < nb[s]) values(s, i, v);
+                        if (ok && i + 1 < nb[s] && wait_seq(k)) {
+                            tc_fence_after();
+                            scores(s, k);
+                        }
+                    }
+                    if (!ok) break;
+                    free_seq(v);
+                    if (k >= 0) free_seq(k);
+                }
+            }
+            if (!ok) {
+                tc_commit(drain);
+                mbar_drain(drain, 0);
+            }
+        }
+        __syncwarp();
+    } else {  // ------------------------------------------------------ softmax
+        const int s = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
+        const uint32_t at = (uint32_t)(quad * 32) << 16;
+        const uint32_t S = tmem + s * 128 + at, O = tmem + 256 + s * HD + at;
+        const int tok = tile[s] * a.tq + row / a.r;
+        const bool live = row < a.tq * a.r && tok < a.n;
+        const bool any = __any_sync(0xffffffffu, live);  // else the warp only keeps the barriers going
+        const int seen = a.kv_len + tok + 1;             // positions this row sees
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int i = 0; i < nb[s]; ++i) {
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(sbar + 8 * s, i & 1, dead)))) break;
+            if (any) {
+                tc_fence_after();
+                uint32_t z[kKeys];
+#pragma unroll
+                for (int c = 0; c < kKeys; c += 32) tmem_ld32(S + c, z + c);
+                tmem_wait_ld();
+                const int left = seen - (lo + (a.shared ? 2 * i + s : i)) * kKeys;  // keys of this block it sees
+                if (__any_sync(0xffffffffu, left < kKeys)) {
+#pragma unroll
+                    for (int c = 0; c < kKeys; ++c)
+                        if (c >= left) z[c] = 0xff800000u;
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < kKeys; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(z[c]));
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+                // m is the reference in log2 units; -inf while the row has seen nothing
+                const bool grow = top > m + kLazy || (m == -INFINITY && top > -INFINITY);
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float to = grow ? top : m;
+                    const float f = m == -INFINITY ? 0.f : ex2(m - to);
+                    l *= f;
+                    m = to;
+                    if (i > 0) {
+#pragma unroll
+                        for (int c = 0; c < HD; c += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(O + c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                            tmem_st32(O + c, o);
+                        }
+                    }
+                }
+                const float ref = m == -INFINITY ? 0.f : -m;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < kKeys; c += 32) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float e0 = ex2(fmaf(__uint_as_float(z[c + 2 * j]), a.scale_log2, ref));
+                        const float e1 = ex2(fmaf(__uint_as_float(z[c + 2 * j + 1]), a.scale_log2, ref));
+                        sum[j & 1] += e0;
+                        sum[2 + (j & 1)] += e1;
+                        p[j] = Half2<T>::pack(e0, e1);
+                    }
+                    tmem_st16(S + c / 2, p);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_wait_st();
+                tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(pbar + 8 * s);
+        }
+        if (ok && nb[s] > 0) ok = __all_sync(0xffffffffu, mbar_wait(obar + 8 * s, 0, dead));
+        // the partial outputs go where the blocks were: the other stream has to be done too
+        if (ok && a.shared && nb[s ^ 1] > 0) ok = __all_sync(0xffffffffu, mbar_wait(obar + 8 * (s ^ 1), 0, dead));
+        tc_fence_after();
+        if (!a.shared) {
+            if (ok && any && nb[s] > 0) {
+                const float inv = 1.f / l;
+                T* out = (T*)a.out + (int64_t)tok * a.out_token + (int64_t)(g * a.r + row % a.r) * a.out_head;
+#pragma unroll
+                for (int c = 0; c < HD; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(O + c, o);
+                    tmem_wait_ld();
+                    if (live) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                w[e] = Half2<T>::pack(__uint_as_float(o[j + 2 * e]) * inv, __uint_as_float(o[j + 2 * e + 1]) * inv);
+                            *reinterpret_cast<uint4*>(out + c + j) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                }
+            }
+        } else {  // leave (m, l, o) for the join; the ring is free: every copy has been used
+            stat[s * 256 + row] = m;
+            stat[s * 256 + 128 + row] = l;
+            if (ok && any && nb[s] > 0) {
+                float* part = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw))) + (s * 128 + row) * kPart;
+#pragma unroll
+                for (int c = 0; c < HD; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(O + c, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) *reinterpret_cast<uint4*>(part + c + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                }
+            }
+        }
+        tc_fence_before();
+    }
+
+    if (a.shared) {
+        // join: a warp per row; lane holds HD / 32 neighbouring outputs
+        __syncwarp();
+        if (a.splits > 1) cluster_sync_all();
+        else __syncthreads();
+        if (!*dead && warp < 8) {
+            const int tokens = min(a.tq, a.n - tile[0] * a.tq), rows = tokens * a.r;
+            constexpr int E = HD / 32;
+            for (int row = rank * 8 + warp; row < rows; row += 8 * a.splits) {
+                float best = -INFINITY;
+                for (int p = 0; p < 2 * a.splits; ++p)
+                    best = fmaxf(best, ld_cluster_f32(map_rank(stat_at + ((p & 1) * 256 + row) * 4, p >> 1)));
+                float l = 0.f, o[E];
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] = 0.f;
+                for (int p = 0; p < 2 * a.splits; ++p) {
+                    const float m = ld_cluster_f32(map_rank(stat_at + ((p & 1) * 256 + row) * 4, p >> 1));
+                    if (m == -INFINITY) continue;  // saw nothing: its output was never written
+                    const float w = ex2(m - best);
+                    l += w * ld_cluster_f32(map_rank(stat_at + ((p & 1) * 256 + 128 + row) * 4, p >> 1));
+                    const uint32_t src = map_rank(ring + (((p & 1) * 128 + row) * kPart + lane * E) * 4, p >> 1);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) o[e] += w * ld_cluster_f32(src + 4 * e);
+                }
+                const float inv = 1.f / l;
+                T* out = (T*)a.out + (int64_t)(tile[0] * a.tq + row / a.r) * a.out_token +
+                         (int64_t)(g * a.r + row % a.r) * a.out_head + lane * E;
+#pragma unroll
+                for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(out + e) = Half2<T>::pack(o[e] * inv, o[e + 1] * inv);
+            }
+        }
+        __syncwarp();
+        if (a.splits > 1) cluster_sync_all();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9) tmem_free<1>(tmem, 512);
+}
+
+template <int HD, typename T>
+int launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, int grid, cudaStream_t s) {
+    constexpr int smem = Shape<HD>::smem;
+    static std::atomic<bool> ready[64];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 64 || !ready[dev].load()) {
+        cudaError_t e = cudaFuncSetAttribute(attention_kernel<HD, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return op_fail(KD_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+        if (dev < 64) ready[dev].store(true);
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThr);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    if (a.splits > 1) {
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = a.splits;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+    }
+    cudaError_t e = cudaLaunchKernelEx(&cfg, attention_kernel<HD, T>, q, k, v, a);
+    if (e != cudaSuccess) return op_fail(KD_ECUDA, "launch failed: %s", cudaGetErrorString(e));
+    return KD_OK;
+}
+
+}  // namespace
+
+int attention_status(cudaStream_t s, unsigned int* st) {
+    cudaError_t e = cudaMemcpyFromSymbolAsync(st, g_op_status, sizeof *st, 0, cudaMemcpyDeviceToHost, s);
+    const unsigned int zero = 0;
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e == cudaSuccess && *st) {
+        e = cudaMemcpyToSymbolAsync(g_op_status, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, s);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    }
+    return e == cudaSuccess ? KD_OK : op_fail(KD_ECUDA, "kd_op_sync: %s", cudaGetErrorString(e));
+}
+
+}  // namespace kd
+
+using namespace kd;
+
+extern "C" int kd_prompt_attention(const kd_attention_args* p, void* stream) {
+    if (!p) return op_fail(KD_EINVAL, "kd_prompt_attention: NULL arguments");
+    kd_attention_args q = *p;
+    if (q.dtype != KD_BF16 && q.dtype != KD_F16)
+        return op_fail(KD_EINVAL, "kd_prompt_attention: dtype must be KD_BF16 or KD_F16");
+    if (q.head_dim != 64 && q.head_dim != 128) return op_fail(KD_EINVAL, "kd_prompt_attention: head_dim must be 64 or 128");
+    if (q.n_heads < 1 || q.n_kv_heads < 1 || q.n_heads % q.n_kv_heads || q.n_heads / q.n_kv_heads > 128 || q.n_kv_heads > 65535)
+        return op_fail(KD_EINVAL, "kd_prompt_attention: %d query heads over %d kv heads (need a multiple, at most 128 each)",
+                       q.n_heads, q.n_kv_heads);
+    if (q.n < 0 || q.kv_len < 0 || q.n > (1 << 30) || q.kv_len > (1 << 30) - q.n)
+        return op_fail(KD_EINVAL, "kd_prompt_attention: n=%lld kv_len=%lld out of range", (long long)q.n, (long long)q.kv_len);
+    if (!(q.scale > 0.f) || !(q.scale < INFINITY)) return op_fail(KD_EINVAL, "kd_prompt_attention: scale must be finite and > 0");
+    if (q.n == 0) return KD_OK;
+    // the stride of a dimension of one entry is not used
+    if (q.n_heads == 1) q.q_head = q.out_head = q.head_dim;
+    if (q.n_kv_heads == 1) q.k_head = q.v_head = q.head_dim;
+    if (q.n == 1) q.q_token = q.out_token = q.head_dim;
+    if (q.n + q.kv_len == 1) q.k_pos = q.v_pos = q.head_dim;
+    const void* ptr[4] = {q.q, q.k, q.v, q.out};
+    const int64_t st[8] = {q.q_token, q.q_head, q.k_pos, q.k_head, q.v_pos, q.v_head, q.out_token, q.out_head};
+    const char* names[4] = {"q", "k", "v", "out"};
+    for (int i = 0; i < 4; ++i) {
+        if (!ptr[i] || ((uintptr_t)ptr[i] & 15))
+            return op_fail(KD_EINVAL, "kd_prompt_attention: %s is NULL or not 16-byte aligned", names[i]);
+        for (int j = 0; j < 2; ++j)
+            if (st[2 * i + j] < q.head_dim || st[2 * i + j] % 8 || st[2 * i + j] >= (int64_t)1 << 38)
+                return op_fail(KD_EINVAL, "kd_prompt_attention: %s: strides must be multiples of 8, at least head_dim", names[i]);
+    }
+    int sms = 0;
+    int rc = op_sm_count(&sms);
+    if (rc) return rc;
+    AttnArgs a{};
+    a.n = (int)q.n, a.kv_len = (int)q.kv_len;
+    a.hkv = q.n_kv_heads, a.r = q.n_heads / q.n_kv_heads;
+    a.tq = 128 / a.r;
+    a.tiles = (a.n + a.tq - 1) / a.tq;
+    a.scale_log2 = q.scale * 1.4426950408889634f;
+    a.out = q.out, a.out_token = q.out_token, a.out_head = q.out_head;
+    const int64_t T = q.kv_len + q.n, units = (int64_t)a.tiles * a.hkv;
+    const int64_t blocks = (T + kKeys - 1) / kKeys;
+    if (units > 0x3fffffff) return op_fail(KD_EINVAL, "kd_prompt_attention: too many tiles");
+    // Few tiles: one tile per CTA, its blocks split over its two streams and over a cluster of
+    // CTAs as long as the SMs last and a CTA keeps two blocks.
+    int64_t grid;
+    a.splits = 1;
+    if (units <= sms) {
+        a.shared = 1;
+        while (a.splits < 8 && units * a.splits * 2 <= sms && blocks >= a.splits * 4) a.splits *= 2;
+        grid = units * a.splits;
+    } else {
+        grid = (int64_t)((a.tiles + 1) / 2) * a.hkv;
+    }
+    CUtensorMap mq, mk, mv;
+    // Rows past the last position read as zeros (not what the cache holds there): a weight of 0
+    // times it is then 0.
+    if ((rc = make_map_3d(&mq, q.dtype, q.q, q.head_dim, q.n_heads, q.n, q.q_head, q.q_token, 64, a.r, a.tq))) return rc;
+    if ((rc = make_map_3d(&mk, q.dtype, q.k, q.head_dim, T, a.hkv, q.k_pos, q.k_head, 64, kKeys, 1))) return rc;
+    if ((rc = make_map_3d(&mv, q.dtype, q.v, q.head_dim, T, a.hkv, q.v_pos, q.v_head, 64, kKeys, 1))) return rc;
+    const bool bf = q.dtype == KD_BF16;
+    a.idesc_s = make_idesc(128, kKeys, bf, false, false);
+    a.idesc_o = make_idesc(128, q.head_dim, bf, false, true);
+    cudaStream_t s = (cudaStream_t)stream;
+    if (q.head_dim == 128)
+        return bf ? launch<128, __nv_bfloat16>(mq, mk, mv, a, (int)grid, s) : launch<128, __half>(mq, mk, mv, a, (int)grid, s);
+    return bf ? launch<64, __nv_bfloat16>(mq, mk, mv, a, (int)grid, s) : launch<64, __half>(mq, mk, mv, a, (int)grid, s);
+}

@@ -611,10 +611,11 @@ extern "C" {
 const char* kd_op_error(void) { return t_err; }
 
 int kd_op_sync(void* stream) {
-    unsigned int a = 0;
+    unsigned int a = 0, b = 0;
     int rc = gemm_status((cudaStream_t)stream, &a);
+    if (rc == KD_OK) rc = attention_status((cudaStream_t)stream, &b);
     if (rc) return rc;
-    if (a) return op_fail(KD_ETIMEOUT, "a device-side wait of an operator exceeded its limit");
+    if (a | b) return op_fail(KD_ETIMEOUT, "a device-side wait of an operator exceeded its limit");
     return KD_OK;
 }
 

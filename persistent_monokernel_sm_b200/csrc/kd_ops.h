@@ -4,5 +4,7 @@
 #include <cuda_runtime.h>
 
 namespace kd {
-int gemm_status(cudaStream_t s, unsigned int* st);  // kd_gemm.cu's status word, cleared
+// The status word of kd_gemm.cu / kd_attention.cu, which is cleared.
+int gemm_status(cudaStream_t s, unsigned int* st);
+int attention_status(cudaStream_t s, unsigned int* st);
 }  // namespace kd

@@ -16,13 +16,14 @@ import torch
 
 from . import KdError, load_library
 
-__all__ = ["linear", "gated_ffn", "gated_ffn_backward"]
+__all__ = ["linear", "gated_ffn", "gated_ffn_backward", "prompt_attention"]
 
 _DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _ACT = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3}
 # the C structs of kd.h, field by field
 _LINEAR = struct.Struct("@4i3qPqPqPPqPq")
 _GATED = struct.Struct("@2i3qPqPqPq")
+_ATTENTION = struct.Struct("@4i2q" + "P2q" * 4 + "fi")
 _EINVAL = -1
 
 
@@ -146,3 +147,38 @@ def gated_ffn_backward(x, wg, wu, dh, act="silu"):
     _enqueue(device, lib.kd_gated_ffn_backward, args, dh.data_ptr(), ldh, dx.data_ptr(), d, dwg.data_ptr(), d,
              dwu.data_ptr(), d, ws.data_ptr(), n)
     return dx, dwg, dwu
+
+
+def prompt_attention(q, k, v, kv_len, scale=None, out=None):
+    """Causal attention of the n new tokens q [n, heads, hd] over a cache k, v [kv_heads, S, hd].
+
+    The cache holds kv_len earlier positions and the n new ones (S >= kv_len + n); token i sees
+    the positions up to kv_len + i. scale: 1 / sqrt(hd) unless given. v has to be finite at
+    all kv_len + n positions; what lies behind them is not read."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.device.type != "cuda":
+        _refuse("q must be a 3-D CUDA tensor [n, heads, head_dim]")
+    dtype, device = q.dtype, q.device
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        _refuse("q must be bfloat16 or float16: got %s" % (dtype,))
+    n, hq, hd = q.shape
+    kv_len = int(kv_len)
+    for name, t in (("k", k), ("v", v)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.dtype is not dtype or t.device != device:
+            _refuse("%s must be a 3-D %s tensor on %s" % (name, dtype, device))
+        if t.shape[2] != hd or t.shape[0] != k.shape[0] or t.shape[1] < kv_len + n:
+            _refuse("%s has shape %s: need [%d, >= %d, %d]" % (name, tuple(t.shape), k.shape[0], kv_len + n, hd))
+    if out is None:
+        out = torch.empty((n, hq, hd), dtype=dtype, device=device)
+    elif out.shape != q.shape or out.dtype is not dtype or out.device != device:
+        _refuse("out must be a %s tensor of q's shape on %s" % (dtype, device))
+    if kv_len < 0:
+        _refuse("kv_len must not be negative")
+    if scale is None:
+        scale = hd ** -0.5
+    qs, ks, vs, os = q.stride(), k.stride(), v.stride(), out.stride()
+    if qs[2] != 1 or ks[2] != 1 or vs[2] != 1 or os[2] != 1:
+        _refuse("the last dimension must be contiguous")
+    _enqueue(device, load_library().kd_prompt_attention,
+             _ATTENTION.pack(_DTYPE[dtype], hq, k.shape[0], hd, n, kv_len, q.data_ptr(), qs[0], qs[1], k.data_ptr(),
+                             ks[1], ks[0], v.data_ptr(), vs[1], vs[0], out.data_ptr(), os[0], os[1], scale, 0))
+    return out
