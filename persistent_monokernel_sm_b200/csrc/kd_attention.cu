@@ -32,7 +32,10 @@
 namespace kd {
 namespace {
 
-constexpr int kThr = 320;   // two warpgroups of softmax, the producer's warp, the issuer's warp
+// Two warpgroups of softmax and one with the producer's and the issuer's warp, which gives the
+// others registers: 256 x 216 + 128 x 72 = 384 x 168, the launch's total.
+constexpr int kThr = 384;
+constexpr int kRowRegs = 216, kAuxRegs = 72;
 constexpr int kKeys = 128;  // positions per block
 constexpr float kLazy = 8.f;
 
@@ -136,7 +139,9 @@ __global__ void __launch_bounds__(kThr, 1)
     tc_fence_after();
     const uint32_t tmem = s_tmem;  // columns: S0, S1 (128 each), O0, O1 (HD each)
 
-    if (warp == 8) {  // ---------------------------------------------- producer
+    if (warp >= 8) {
+      set_regs_down<kAuxRegs>();
+      if (warp == 8) {  // ---------------------------------------------- producer
         if (lane == 0) {
             const int two = !a.shared && tile[1] < a.tiles ? 2 : 1;
             mbar_expect(qbar, two * kHalves * a.tq * a.r * 128);
@@ -236,7 +241,18 @@ __global__ void __launch_bounds__(kThr, 1)
             }
         }
         __syncwarp();
+      }
+      if (a.shared) {  // the join's meetings
+          __syncwarp();
+          if (a.splits > 1) {
+              cluster_sync_all();
+              cluster_sync_all();
+          } else {
+              __syncthreads();
+          }
+      }
     } else {  // ------------------------------------------------------ softmax
+        set_regs_up<kRowRegs>();
         const int s = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
         const uint32_t at = (uint32_t)(quad * 32) << 16;
         const uint32_t S = tmem + s * 128 + at, O = tmem + 256 + s * HD + at;
@@ -346,41 +362,40 @@ __global__ void __launch_bounds__(kThr, 1)
             }
         }
         tc_fence_before();
-    }
-
-    if (a.shared) {
-        // join: a warp per row; lane holds HD / 32 neighbouring outputs
-        __syncwarp();
-        if (a.splits > 1) cluster_sync_all();
-        else __syncthreads();
-        if (!*dead && warp < 8) {
-            const int tokens = min(a.tq, a.n - tile[0] * a.tq), rows = tokens * a.r;
-            constexpr int E = HD / 32;
-            for (int row = rank * 8 + warp; row < rows; row += 8 * a.splits) {
-                float best = -INFINITY;
-                for (int p = 0; p < 2 * a.splits; ++p)
-                    best = fmaxf(best, ld_cluster_f32(map_rank(stat_at + ((p & 1) * 256 + row) * 4, p >> 1)));
-                float l = 0.f, o[E];
-#pragma unroll
-                for (int e = 0; e < E; ++e) o[e] = 0.f;
-                for (int p = 0; p < 2 * a.splits; ++p) {
-                    const float m = ld_cluster_f32(map_rank(stat_at + ((p & 1) * 256 + row) * 4, p >> 1));
-                    if (m == -INFINITY) continue;  // saw nothing: its output was never written
-                    const float w = ex2(m - best);
-                    l += w * ld_cluster_f32(map_rank(stat_at + ((p & 1) * 256 + 128 + row) * 4, p >> 1));
-                    const uint32_t src = map_rank(ring + (((p & 1) * 128 + row) * kPart + lane * E) * 4, p >> 1);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) o[e] += w * ld_cluster_f32(src + 4 * e);
+        if (a.shared) {
+            // join: a warp per row; lane holds HD / 32 neighbouring outputs
+            __syncwarp();
+            if (a.splits > 1) cluster_sync_all();
+            else __syncthreads();
+            if (!*dead) {
+                const int tokens = min(a.tq, a.n - tile[0] * a.tq), rows = tokens * a.r;
+                constexpr int E = HD / 32;
+                for (int row = rank * 8 + warp; row < rows; row += 8 * a.splits) {
+                    float best = -INFINITY;
+                    for (int p = 0; p < 2 * a.splits; ++p)
+                        best = fmaxf(best, ld_cluster_f32(map_rank(stat_at + ((p & 1) * 256 + row) * 4, p >> 1)));
+                    float l = 0.f, o[E];
+    #pragma unroll
+                    for (int e = 0; e < E; ++e) o[e] = 0.f;
+                    for (int p = 0; p < 2 * a.splits; ++p) {
+                        const float m = ld_cluster_f32(map_rank(stat_at + ((p & 1) * 256 + row) * 4, p >> 1));
+                        if (m == -INFINITY) continue;  // saw nothing: its output was never written
+                        const float w = ex2(m - best);
+                        l += w * ld_cluster_f32(map_rank(stat_at + ((p & 1) * 256 + 128 + row) * 4, p >> 1));
+                        const uint32_t src = map_rank(ring + (((p & 1) * 128 + row) * kPart + lane * E) * 4, p >> 1);
+    #pragma unroll
+                        for (int e = 0; e < E; ++e) o[e] += w * ld_cluster_f32(src + 4 * e);
+                    }
+                    const float inv = 1.f / l;
+                    T* out = (T*)a.out + (int64_t)(tile[0] * a.tq + row / a.r) * a.out_token +
+                             (int64_t)(g * a.r + row % a.r) * a.out_head + lane * E;
+    #pragma unroll
+                    for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(out + e) = Half2<T>::pack(o[e] * inv, o[e + 1] * inv);
                 }
-                const float inv = 1.f / l;
-                T* out = (T*)a.out + (int64_t)(tile[0] * a.tq + row / a.r) * a.out_token +
-                         (int64_t)(g * a.r + row % a.r) * a.out_head + lane * E;
-#pragma unroll
-                for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(out + e) = Half2<T>::pack(o[e] * inv, o[e + 1] * inv);
             }
+            __syncwarp();
+            if (a.splits > 1) cluster_sync_all();
         }
-        __syncwarp();
-        if (a.splits > 1) cluster_sync_all();
     }
     tc_fence_before();
     __syncthreads();

@@ -105,7 +105,15 @@ int make_map_3d(CUtensorMap* m, int dtype, const void* base, int64_t c0, int64_t
 
 namespace {
 
-constexpr int kGemmThreads = 320;  // 8 epilogue warps, the producer's warp, the issuer's warp
+// Three warpgroups: two of epilogue warps, one with the producer's and the issuer's warp. The
+// epilogue takes registers from the third: 256 x 216 + 128 x 72 = 384 x 168, the launch's total.
+constexpr int kGemmThreads = 384;
+constexpr int kEpiRegs = 216, kAuxRegs = 72;
+// An accumulator of the tensor cores is truncated at every step of 16 products (measured:
+// 1.7e-8 relative per step, all towards zero, 4.3e-6 at k = 4,096). Where the result is kept in
+// fp32, sums of more than 512 products are therefore taken as several, added in registers with
+// rounding to nearest. A 16-bit result does not show it (2^-9 and 2^-12).
+constexpr int kChunk = 8;  // k-blocks
 constexpr int kBK = 64;            // k-block: 128 bytes of a row
 constexpr int kABytes = 128 * kBK * 2;
 constexpr int kMaxRing = 12;
@@ -239,6 +247,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_dead;
 
+    constexpr bool kSums = EPI == EPI_LINEAR && sizeof(O) == 4;  // add sums of kStep k-blocks
+    constexpr int kStep = kSums ? kChunk : 1 << 28;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t ring = (smem_u32(smem_raw) + 1023) & ~1023u;
     const int bbytes = g.bn * kBK * 2, sbytes = kABytes + bbytes;
@@ -279,7 +289,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         tt = grp * kGroup + in % size;
     };
 
-    if (warp == 8) {  // ---------------------------------------------- producer
+    if (warp >= 8) {
+      set_regs_down<kAuxRegs>();
+      if (warp == 8) {  // ---------------------------------------------- producer
         if (lane == 0) {
             int it = 0;
             bool ok = true;
@@ -325,14 +337,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if (lane == 0) {
             const uint32_t a_lbo = g.a_mn ? 8192 : 16, b_lbo = g.b_mn ? 8192 : 16;
             const uint64_t a_step = g.a_mn ? 2048 >> 4 : 32 >> 4, b_step = g.b_mn ? 2048 >> 4 : 32 >> 4;
-            int it = 0, local = 0;
+            int it = 0, local = 0;  // k-blocks and accumulators so far
             bool ok = true;
-            for (int tile = first; tile < tiles && ok; tile += step, ++local) {
-                const int buf = local & 1;
+            for (int tile = first; tile < tiles && ok; tile += step)
+              for (int c_lo = k_lo; c_lo < k_hi && ok; c_lo += kStep, ++local) {
+                const int buf = local & 1, c_hi = min(k_hi, c_lo + kStep);
                 if (!(ok = mbar_wait(tempty + 8 * buf, ((local >> 1) & 1) ^ 1, dead))) break;
                 tc_fence_after();
                 const uint32_t d = tmem + buf * g.bn;
-                for (int kb = k_lo; kb < k_hi; ++kb, ++it) {
+                for (int kb = c_lo; kb < c_hi; ++kb, ++it) {
                     const int st = it % g.stages, ph = (it / g.stages) & 1;
                     if (!(ok = mbar_wait(full + 8 * st, ph, dead))) break;
                     tc_fence_after();
@@ -340,7 +353,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     const uint64_t da = make_desc(sa, a_lbo, 1024), db = make_desc(sb, b_lbo, 1024);
 #pragma unroll
                     for (int ks = 0; ks < kBK / 16; ++ks)
-                        mma_ss<1>(d, da + ks * a_step, db + ks * b_step, g.idesc, kb > k_lo || ks > 0);
+                        mma_ss<1>(d, da + ks * a_step, db + ks * b_step, g.idesc, kb > c_lo || ks > 0);
                     tc_commit(empty + 8 * st);
                 }
                 if (ok) tc_commit(tfull + 8 * buf);
@@ -351,11 +364,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             }
         }
         __syncwarp();
+      }
+      if (g.splits > 1) {  // the epilogue's two meetings of the cluster
+          __syncwarp();
+          cluster_sync_all();
+          cluster_sync_all();
+      }
     } else {  // ------------------------------------------------------ epilogue
+        set_regs_up<kEpiRegs>();
         const int quad = warp & 3, half = warp >> 2;
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         int local = 0;
-        for (int tile = first; tile < tiles; tile += step, ++local) {
-            const int buf = local & 1;
+        bool ok = true;
+        for (int tile = first; tile < tiles && ok; tile += step) {
             int tn, tt;
             place(tile, tn, tt);
             float bias = 0.f;
@@ -363,69 +384,101 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 const int64_t n = (int64_t)tn * 128 + quad * 32 + lane;
                 if (g.bias && n < g.N) bias = to_f<T>(((const T*)g.bias)[n]);
             }
-            if (!__all_sync(0xffffffffu, mbar_wait(tfull + 8 * buf, (local >> 1) & 1, dead))) break;
-            tc_fence_after();
-            const uint32_t src = tmem + buf * g.bn + ((uint32_t)(quad * 32) << 16);
             const int64_t t0 = (int64_t)tt * g.bn;
             const int valid = (int)min((int64_t)g.bn, g.M - t0);
-            if (g.splits > 1) {  // the partial tile, [token][feature], for the cluster to sum
-                float* part = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)));
-                for (int c = half * 16; c < valid; c += 32) {
-                    uint32_t r[16];
-                    tmem_ld16(src + c, r);
-                    tmem_wait_ld();
+            // columns of this warp: blocks of 32 (16 in the narrowest tile), every other one
+            auto finish = [&](int c, const float* v) {
+                if (g.splits > 1) {  // the partial tile, [token][feature], for the cluster to sum
+                    float* part = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)));
+                    const int n = g.bn >= 32 ? 32 : 16;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) part[(c + j) * 128 + quad * 32 + lane] = __uint_as_float(r[j]);
+                    for (int j = 0; j < 32; ++j)
+                        if (j < n) part[(c + j) * 128 + quad * 32 + lane] = v[j];
+                } else if (g.bn >= 32) {
+                    emit_act<EPI, 32, T, O>(g, v, tn, quad, lane, t0 + c, bias);
+                } else {
+                    emit_act<EPI, 16, T, O>(g, v, tn, quad, lane, t0 + c, bias);
+                }
+            };
+            auto fetch = [&](uint32_t src, uint32_t* r) {
+                if (g.bn >= 32) tmem_ld32(src, r);
+                else tmem_ld16(src, r);
+                tmem_wait_ld();
+            };
+            if constexpr (kSums) {
+                float acc[4][32];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) acc[i][j] = 0.f;
+                for (int c_lo = k_lo; c_lo < k_hi && ok; c_lo += kStep, ++local) {
+                    const int buf = local & 1;
+                    if (!(ok = __all_sync(0xffffffffu, mbar_wait(tfull + 8 * buf, (local >> 1) & 1, dead)))) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int c = half * 32 + 64 * i;
+                        if (c >= valid) break;
+                        uint32_t r[32];
+                        fetch(tmem + buf * g.bn + lanes + c, r);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) acc[i][j] += __uint_as_float(r[j]);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(tempty + 8 * buf);
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int c = half * 32 + 64 * i;
+                    if (c >= valid) break;
+                    finish(c, acc[i]);
                 }
             } else {
+                const int buf = local & 1;
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(tfull + 8 * buf, (local >> 1) & 1, dead)))) break;
+                tc_fence_after();
                 for (int c = half * 32; c < valid; c += 64) {
-                    if (g.bn >= 32) {
-                        uint32_t r[32];
-                        tmem_ld32(src + c, r);
-                        tmem_wait_ld();
-                        emit_act<EPI, 32, T, O>(g, reinterpret_cast<const float*>(r), tn, quad, lane, t0 + c, bias);
-                    } else {
-                        uint32_t r[16];
-                        tmem_ld16(src + c, r);
-                        tmem_wait_ld();
-                        emit_act<EPI, 16, T, O>(g, reinterpret_cast<const float*>(r), tn, quad, lane, t0 + c, bias);
-                    }
+                    uint32_t r[32];
+                    fetch(tmem + buf * g.bn + lanes + c, r);
+                    finish(c, reinterpret_cast<const float*>(r));
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(tempty + 8 * buf);
+                ++local;
             }
-            tc_fence_before();
+        }
+        if (g.splits > 1) {
             __syncwarp();
-            if (lane == 0) mbar_arrive(tempty + 8 * buf);
-        }
-    }
-
-    if (g.splits > 1) {
-        __syncwarp();
-        cluster_sync_all();
-        if (warp < 8 && !*dead) {
-            int tn, tt;
-            place(first, tn, tt);
-            const int64_t t0 = (int64_t)tt * g.bn;
-            const int valid = (int)min((int64_t)g.bn, g.M - t0);
-            const int pairs = (valid + 1) / 2;
-            for (int u = rank * 8 + warp; u < 4 * pairs; u += 8 * g.splits) {
-                const int quad = u & 3, c = (u >> 2) * 2;
-                float v[2] = {0.f, 0.f};
-                const uint32_t at = ring + (uint32_t)(c * 128 + quad * 32 + lane) * 4;
-                for (int s = 0; s < g.splits; ++s) {
-                    const uint32_t ra = map_rank(at, s);
-                    v[0] += ld_cluster_f32(ra);
-                    v[1] += ld_cluster_f32(ra + 512);
+            cluster_sync_all();
+            if (!*dead) {
+                int tn, tt;
+                place(first, tn, tt);
+                const int64_t t0 = (int64_t)tt * g.bn;
+                const int valid = (int)min((int64_t)g.bn, g.M - t0);
+                const int pairs = (valid + 1) / 2;
+                for (int u = rank * 8 + warp; u < 4 * pairs; u += 8 * g.splits) {
+                    const int quad = u & 3, c = (u >> 2) * 2;
+                    float v[2] = {0.f, 0.f};
+                    const uint32_t at = ring + (uint32_t)(c * 128 + quad * 32 + lane) * 4;
+                    for (int s = 0; s < g.splits; ++s) {
+                        const uint32_t ra = map_rank(at, s);
+                        v[0] += ld_cluster_f32(ra);
+                        v[1] += ld_cluster_f32(ra + 512);
+                    }
+                    float bias = 0.f;
+                    if constexpr (EPI == EPI_LINEAR) {
+                        const int64_t n = (int64_t)tn * 128 + quad * 32 + lane;
+                        if (g.bias && n < g.N) bias = to_f<T>(((const T*)g.bias)[n]);
+                    }
+                    emit_act<EPI, 2, T, O>(g, v, tn, quad, lane, t0 + c, bias);
                 }
-                float bias = 0.f;
-                if constexpr (EPI == EPI_LINEAR) {
-                    const int64_t n = (int64_t)tn * 128 + quad * 32 + lane;
-                    if (g.bias && n < g.N) bias = to_f<T>(((const T*)g.bias)[n]);
-                }
-                emit_act<EPI, 2, T, O>(g, v, tn, quad, lane, t0 + c, bias);
             }
+            __syncwarp();
+            cluster_sync_all();
         }
-        __syncwarp();
-        cluster_sync_all();
     }
     tc_fence_before();
     __syncthreads();
