@@ -134,6 +134,23 @@ int kd_set_kv(kd_ctx *ctx, int32_t layer, int32_t which, const void *d_src, int3
  * run that kd_sync reported. */
 int kd_reset(kd_ctx *ctx, const int32_t *d_tokens, int32_t n_tokens, int32_t kv_len);
 
+/* Start a request with its prompt run through the layers at once, instead of token by token in
+ * kd_decode: positions [0, kv_len) of the cache are taken as valid, the K and V rows of all but
+ * the last of the n_tokens ids at d_tokens (device memory, n_tokens >= 1) are appended at
+ * kv_len, kv_len + 1, ..., and the last token is left pending at kv_len + n_tokens - 1, so that
+ * kd_decode continues from there. Runs on the handle's stream with the prompt operators below,
+ * straight from the arena's weights; d_tokens and the workspace (device memory, used while the
+ * call's kernels run) may go away once the stream has passed the call. With a workspace of
+ * kd_prefill_workspace() bytes for n_tokens the prompt goes through in one piece; a smaller one
+ * means several, one that does not hold a single token KD_ENOMEM. kv_len + n_tokens > max_seq:
+ * KD_ECAPACITY. A token id outside [0, vocab) is reported by kd_sync (KD_ETOKEN).
+ * Operands of the tensor cores (normalised activations, q, attention outputs, hidden units) are
+ * rounded to bf16; kd_decode keeps those in fp32, so the cache differs from the one it would
+ * have written by such roundings. */
+size_t kd_prefill_workspace(const kd_config *cfg, int32_t n_tokens);
+int kd_prefill(kd_ctx *ctx, const int32_t *d_tokens, int32_t n_tokens, int32_t kv_len, void *workspace,
+               size_t workspace_bytes);
+
 /* Run the pending tokens through the decoder, then generate n_gen tokens greedily, in ONE
  * kernel launch. Steps run = pending + n_gen - 1; each appends one KV position.
  * d_tokens_out: device int32 [n_gen] (may be NULL only if n_gen == 0).

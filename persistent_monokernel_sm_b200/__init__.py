@@ -18,6 +18,7 @@ __all__ = ["KdError", "kd_config", "kd_weights", "kd_info", "load_library", "Dec
            "kd_last_error", "kd_strerror", "kd_destroy", "LIB_PATH", "ERRORS",
            "kd_linear_args", "kd_gated_args", "kd_linear", "kd_gated_ffn", "kd_gated_ffn_backward_workspace",
            "kd_gated_ffn_backward", "kd_attention_args", "kd_prompt_attention", "kd_op_sync", "kd_op_error",
+           "kd_prefill_workspace", "kd_prefill",
            "linear", "gated_ffn", "gated_ffn_backward", "prompt_attention"]
 
 _OPERATORS = ("linear", "gated_ffn", "gated_ffn_backward", "prompt_attention")
@@ -126,6 +127,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "kd_last_error": (ctypes.c_char_p, [_P]),
         "kd_strerror": (ctypes.c_char_p, [ctypes.c_int]),
         "kd_destroy": (None, [_P]),
+        "kd_prefill_workspace": (ctypes.c_size_t, [_CFG, ctypes.c_int32]),
+        "kd_prefill": (ctypes.c_int, [_P, _P, ctypes.c_int32, ctypes.c_int32, _P, ctypes.c_size_t]),
         # the argument structs of the operators are taken as a pointer or as packed bytes
         "kd_linear": (ctypes.c_int, [ctypes.c_char_p, _P]),
         "kd_gated_ffn": (ctypes.c_int, [ctypes.c_char_p, _P, ctypes.c_int64, _P]),
@@ -177,6 +180,14 @@ def kd_set_kv(h, layer: int, which: int, d_src: int, n_pos: int) -> int:
 
 def kd_reset(h, d_tokens: int, n_tokens: int, kv_len: int) -> int:
     return _check(h, load_library().kd_reset(h, d_tokens, n_tokens, kv_len), "kd_reset")
+
+
+def kd_prefill_workspace(cfg: kd_config, n_tokens: int) -> int:
+    return load_library().kd_prefill_workspace(ctypes.byref(cfg), n_tokens)
+
+
+def kd_prefill(h, d_tokens: int, n_tokens: int, kv_len: int, workspace: int, workspace_bytes: int) -> int:
+    return _check(h, load_library().kd_prefill(h, d_tokens, n_tokens, kv_len, workspace, workspace_bytes), "kd_prefill")
 
 
 def kd_decode(h, n_gen: int, d_tokens_out: int, d_logits_out: int | None) -> int:
@@ -348,6 +359,21 @@ class Decoder:
         self._tokens = t  # kept alive until the copy has run
         kd_reset(self.h, t.data_ptr(), t.numel(), kv_len)
         self.pending = t.numel()
+
+    def prefill(self, tokens, kv_len: int = 0, max_piece: int = 4096):
+        """reset() for a prompt: all but its last token run through the layers now, on the tensor
+        cores, at most max_piece tokens at once; the last one is pending for decode()."""
+        torch = self.torch
+        if max_piece < 1:
+            raise KdError(-1, "prefill: max_piece must be at least 1")
+        with torch.cuda.device(self.device), torch.cuda.stream(self.stream):
+            t = torch.as_tensor(tokens, dtype=torch.int32).to(self.device).contiguous()
+            n = t.numel()
+            nbytes = kd_prefill_workspace(self.cfg, max(1, min(n - 1, max_piece)))
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+            self._tokens = t  # kept alive until the stream has passed
+            kd_prefill(self.h, t.data_ptr(), n, kv_len, ws.data_ptr(), nbytes)
+        self.pending = 1
 
     def decode(self, n_gen: int, logits: bool = False, out=None):
         """Enqueue one decode launch; returns (tokens [n_gen] int32, logits [steps][V] or None)."""

@@ -8,7 +8,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libkd.so")
-SOURCES = ["kd_kernel.cu", "kd_api.cu", "kd_noalloc.cu", "kd_gemm.cu", "kd_attention.cu"]
+SOURCES = ["kd_kernel.cu", "kd_api.cu", "kd_noalloc.cu", "kd_gemm.cu", "kd_attention.cu",
+           "kd_prefill.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
          "-Xcompiler", "-fPIC", "-I" + os.path.join(ROOT, "include"), "-I" + CSRC]

@@ -263,6 +263,12 @@ int kd_internal_fail(kd_ctx* c, int code, const char* msg) { return fail(c, code
 void kd_internal_count_launch(kd_ctx* c) { c->launches += 1; }
 
 namespace kd {
+bool dims_of(const kd_config* cfg, Dims* d) {
+    if (!valid_config(cfg)) return false;
+    *d = make_dims(cfg);
+    return true;
+}
+
 // The launch parameters that depend only on the handle (shared with kd_decode_noalloc).
 void fill_launch_shape(const kd_ctx_view& v, Params& p) {
     p.dm = *v.dm;
