@@ -23,6 +23,7 @@
 #include <string.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "kd.h"
 #include "kd_layout.h"
@@ -113,20 +114,22 @@ constexpr int kEpiRegs = 216, kAuxRegs = 72;
 // 1.7e-8 relative per step, all towards zero, 4.3e-6 at k = 4,096). Where the result is kept in
 // fp32, sums of more than 512 products are therefore taken as several, added in registers with
 // rounding to nearest. A 16-bit result does not show it (2^-9 and 2^-12).
-constexpr int kChunk = 8;  // k-blocks
+constexpr int kChunk = 8;  // 64-deep k-blocks
 constexpr int kBK = 64;            // k-block: 128 bytes of a row
 constexpr int kABytes = 128 * kBK * 2;
 constexpr int kMaxRing = 12;
 constexpr int kRingBytes = 216 * 1024;
 constexpr int kGroup = 8;  // token tiles that are taken together while the weight tiles advance
 
+// Which index of the two operands is the contiguous one in memory: k of both; the feature of A
+// and k of B (a transposed weight); the feature and the token (a sum over rows).
+enum { LAY_KK = 0, LAY_MK = 1, LAY_MM = 2 };
 enum { EPI_LINEAR = 0, EPI_GATED = 1, EPI_GATED_BWD = 2 };
 
 struct GemmArgs {
     int n_tiles, t_tiles;  // tiles over features and tokens
     int kb0, kb;           // k-blocks of the first operand pair, of both
     int bn, stages, splits;
-    int a_mn, b_mn;
     uint32_t idesc;
     int act;
     int64_t N, M;  // features (of the output), tokens
@@ -237,7 +240,7 @@ __device__ __forceinline__ void emit_act(const GemmArgs& g, const float* v, int6
 }
 
 // ------------------------------------------------------------------ the kernel
-template <int EPI, typename T, typename O>
+template <int EPI, int LAY, typename T, typename O>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUtensorMap a1,
                 const __grid_constant__ CUtensorMap b0, const __grid_constant__ CUtensorMap b1,
@@ -247,6 +250,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_dead;
 
+    constexpr bool kAMn = LAY != LAY_KK, kBMn = LAY == LAY_MM;
     constexpr bool kSums = EPI == EPI_LINEAR && sizeof(O) == 4;  // add sums of kStep k-blocks
     constexpr int kStep = kSums ? kChunk : 1 << 28;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -291,70 +295,91 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 
     if (warp >= 8) {
       set_regs_down<kAuxRegs>();
+      // The two roles run in one thread each, and at a few hundred clocks per k-block it is their
+      // instructions that bound the kernel: ring position, phase and descriptors are carried
+      // along, not computed from a count, and the next barrier is looked at ahead of its use.
+      const int stages = g.stages, bn = g.bn;
+      const uint32_t to_empty = empty - full;
       if (warp == 8) {  // ---------------------------------------------- producer
-        if (lane == 0) {
-            int it = 0;
-            bool ok = true;
+        if (elect_one()) {
+            int st = 0, used = 0;
+            uint32_t ph = 1, bar = full, at = ring;
+            bool ok = true, ready = true;  // the ring starts empty
             for (int tile = first; tile < tiles && ok; tile += step) {
                 int tn, tt;
                 place(tile, tn, tt);
-                for (int kb = k_lo; kb < k_hi; ++kb, ++it) {
-                    const int st = it % g.stages, ph = (it / g.stages) & 1;
-                    if (!(ok = mbar_wait(empty + 8 * st, ph ^ 1, dead))) break;
-                    const uint32_t bar = full + 8 * st, sa = ring + st * sbytes, sb = sa + kABytes;
-                    mbar_expect(bar, sbytes);
-                    const bool second = kb >= g.kb0;
-                    const int k = (second ? kb - g.kb0 : kb) * kBK;
-                    if constexpr (EPI == EPI_LINEAR) {
-                        const CUtensorMap* ma = second ? &a1 : &a0;
-                        if (g.a_mn) {
-                            tma_2d<1>(sa, ma, tn * 128, k, bar);
-                            tma_2d<1>(sa + kABytes / 2, ma, tn * 128 + 64, k, bar);
+                const int an = tn * (EPI == EPI_LINEAR ? 128 : 64), bt = tt * bn;
+                int kb = k_lo;
+#pragma unroll
+                for (int seg = 0; seg < 2; ++seg) {  // the first operand pair, the second
+                    const int end = seg ? k_hi : min(g.kb0, k_hi);
+                    const CUtensorMap *ma = seg ? &a1 : &a0, *mb = seg ? &b1 : &b0;
+                    int k = (kb - (seg ? g.kb0 : 0)) * kBK;
+#pragma unroll 1
+                    for (; kb < end && ok; ++kb, k += kBK) {
+                        if (!ready && !(ok = mbar_wait(bar + to_empty, ph, dead))) break;
+                        const uint32_t here = bar, sa = at, sb = at + kABytes;
+                        at += sbytes, bar += 8;
+                        if (++st == stages) st = 0, ph ^= 1, at = ring, bar = full;
+                        ready = mbar_test(bar + to_empty, ph);
+                        mbar_expect(here, sbytes);
+                        if constexpr (EPI != EPI_LINEAR) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                tma_2d<1>(sa + q * 4096, &a0, k, an + q * 16, here);
+                                tma_2d<1>(sa + q * 4096 + 2048, &a1, k, an + q * 16, here);
+                            }
+                        } else if constexpr (kAMn) {
+                            tma_2d<1>(sa, ma, an, k, here);
+                            tma_2d<1>(sa + kABytes / 2, ma, an + 64, k, here);
                         } else {
-                            tma_2d<1>(sa, ma, k, tn * 128, bar);
+                            tma_2d<1>(sa, ma, k, an, here);
                         }
-                    } else {
-                        for (int q = 0; q < 4; ++q) {
-                            tma_2d<1>(sa + q * 4096, &a0, k, tn * 64 + q * 16, bar);
-                            tma_2d<1>(sa + q * 4096 + 2048, &a1, k, tn * 64 + q * 16, bar);
+                        if constexpr (kBMn) {
+                            for (int j = 0; j < bn; j += 64) tma_2d<1>(sb + j * 128, mb, bt + j, k, here);
+                        } else {
+                            tma_2d<1>(sb, mb, k, bt, here);
                         }
-                    }
-                    const CUtensorMap* mb = second ? &b1 : &b0;
-                    if (g.b_mn) {
-                        for (int j = 0; j < g.bn / 64; ++j)
-                            tma_2d<1>(sb + j * 8192, mb, tt * g.bn + j * 64, k, bar);
-                    } else {
-                        tma_2d<1>(sb, mb, k, tt * g.bn, bar);
+                        ++used;
                     }
                 }
             }
             if (!ok)  // let the copies in flight land before the CTA ends
-                for (int i = it > g.stages ? it - g.stages : 0; i < it; ++i)
-                    mbar_drain(full + 8 * (i % g.stages), (i / g.stages) & 1);
+                for (int i = used > stages ? used - stages : 0; i < used; ++i)
+                    mbar_drain(full + 8 * (i % stages), (i / stages) & 1);
         }
         __syncwarp();
-    } else if (warp == 9) {  // --------------------------------------- issuer
-        if (lane == 0) {
-            const uint32_t a_lbo = g.a_mn ? 8192 : 16, b_lbo = g.b_mn ? 8192 : 16;
-            const uint64_t a_step = g.a_mn ? 2048 >> 4 : 32 >> 4, b_step = g.b_mn ? 2048 >> 4 : 32 >> 4;
-            int it = 0, local = 0;  // k-blocks and accumulators so far
-            bool ok = true;
+      } else if (warp == 9) {  // --------------------------------------- issuer
+        if (elect_one()) {
+            const uint64_t a_first = make_desc(ring, kAMn ? 8192 : 16, 1024);
+            const uint64_t b_first = make_desc(ring + kABytes, kBMn ? 8192 : 16, 1024);
+            constexpr uint32_t kAStep = kAMn ? 2048 >> 4 : 32 >> 4, kBStep = kBMn ? 2048 >> 4 : 32 >> 4;
+            const uint32_t idesc = g.idesc, hop = (uint32_t)sbytes >> 4;
+            int st = 0, local = 0;  // local: accumulators so far
+            uint32_t ph = 0, bar = full, off = 0;
+            bool ok = true, ready = false;
             for (int tile = first; tile < tiles && ok; tile += step)
-              for (int c_lo = k_lo; c_lo < k_hi && ok; c_lo += kStep, ++local) {
-                const int buf = local & 1, c_hi = min(k_hi, c_lo + kStep);
+              for (int kb = k_lo; kb < k_hi && ok; ++local) {
+                const int buf = local & 1, c_hi = min(k_hi, kb + kStep);
                 if (!(ok = mbar_wait(tempty + 8 * buf, ((local >> 1) & 1) ^ 1, dead))) break;
                 tc_fence_after();
-                const uint32_t d = tmem + buf * g.bn;
-                for (int kb = c_lo; kb < c_hi; ++kb, ++it) {
-                    const int st = it % g.stages, ph = (it / g.stages) & 1;
-                    if (!(ok = mbar_wait(full + 8 * st, ph, dead))) break;
+                const uint32_t d = tmem + buf * bn;
+                bool add = false;
+#pragma unroll 1
+                for (; kb < c_hi; ++kb) {
+                    if (!ready && !(ok = mbar_wait(bar, ph, dead))) break;
                     tc_fence_after();
-                    const uint32_t sa = ring + st * sbytes, sb = sa + kABytes;
-                    const uint64_t da = make_desc(sa, a_lbo, 1024), db = make_desc(sb, b_lbo, 1024);
+                    const uint64_t da = a_first + off, db = b_first + off;
+                    const uint32_t done = bar + to_empty;
+                    off += hop, bar += 8;
+                    if (++st == stages) st = 0, ph ^= 1, off = 0, bar = full;
+                    ready = mbar_test(bar, ph);
 #pragma unroll
-                    for (int ks = 0; ks < kBK / 16; ++ks)
-                        mma_ss<1>(d, da + ks * a_step, db + ks * b_step, g.idesc, kb > c_lo || ks > 0);
-                    tc_commit(empty + 8 * st);
+                    for (int ks = 0; ks < kBK / 16; ++ks) {
+                        mma_ss<1>(d, da + ks * kAStep, db + ks * kBStep, idesc, add);
+                        add = true;
+                    }
+                    tc_commit(done);
                 }
                 if (ok) tc_commit(tfull + 8 * buf);
             }
@@ -413,7 +438,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     for (int j = 0; j < 32; ++j) acc[i][j] = 0.f;
                 for (int c_lo = k_lo; c_lo < k_hi && ok; c_lo += kStep, ++local) {
                     const int buf = local & 1;
-                    if (!(ok = __all_sync(0xffffffffu, mbar_wait(tfull + 8 * buf, (local >> 1) & 1, dead)))) break;
+                    if (!(ok = mbar_wait_all(tfull + 8 * buf, (local >> 1) & 1, dead))) break;
                     tc_fence_after();
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -437,7 +462,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 }
             } else {
                 const int buf = local & 1;
-                if (!(ok = __all_sync(0xffffffffu, mbar_wait(tfull + 8 * buf, (local >> 1) & 1, dead)))) break;
+                if (!(ok = mbar_wait_all(tfull + 8 * buf, (local >> 1) & 1, dead))) break;
                 tc_fence_after();
                 for (int c = half * 32; c < valid; c += 64) {
                     uint32_t r[32];
@@ -459,22 +484,33 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 const int64_t t0 = (int64_t)tt * g.bn;
                 const int valid = (int)min((int64_t)g.bn, g.M - t0);
                 const int pairs = (valid + 1) / 2;
-                for (int u = rank * 8 + warp; u < 4 * pairs; u += 8 * g.splits) {
-                    const int quad = u & 3, c = (u >> 2) * 2;
-                    float v[2] = {0.f, 0.f};
-                    const uint32_t at = ring + (uint32_t)(c * 128 + quad * 32 + lane) * 4;
-                    for (int s = 0; s < g.splits; ++s) {
-                        const uint32_t ra = map_rank(at, s);
-                        v[0] += ld_cluster_f32(ra);
-                        v[1] += ld_cluster_f32(ra + 512);
+                // Every CTA's share of a pair of columns is asked for before the first is used.
+                auto join = [&](auto count) {
+                    constexpr int S = decltype(count)::value;
+                    for (int u = rank * 8 + warp; u < 4 * pairs; u += 8 * S) {
+                        const int quad = u & 3, c = (u >> 2) * 2;
+                        const uint32_t at = ring + (uint32_t)(c * 128 + quad * 32 + lane) * 4;
+                        float part[S][2];
+#pragma unroll
+                        for (int s = 0; s < S; ++s) {
+                            const uint32_t ra = map_rank(at, s);
+                            part[s][0] = ld_cluster_f32(ra);
+                            part[s][1] = ld_cluster_f32(ra + 512);
+                        }
+                        float v[2] = {part[0][0], part[0][1]};
+#pragma unroll
+                        for (int s = 1; s < S; ++s) v[0] += part[s][0], v[1] += part[s][1];
+                        float bias = 0.f;
+                        if constexpr (EPI == EPI_LINEAR) {
+                            const int64_t n = (int64_t)tn * 128 + quad * 32 + lane;
+                            if (g.bias && n < g.N) bias = to_f<T>(((const T*)g.bias)[n]);
+                        }
+                        emit_act<EPI, 2, T, O>(g, v, tn, quad, lane, t0 + c, bias);
                     }
-                    float bias = 0.f;
-                    if constexpr (EPI == EPI_LINEAR) {
-                        const int64_t n = (int64_t)tn * 128 + quad * 32 + lane;
-                        if (g.bias && n < g.N) bias = to_f<T>(((const T*)g.bias)[n]);
-                    }
-                    emit_act<EPI, 2, T, O>(g, v, tn, quad, lane, t0 + c, bias);
-                }
+                };
+                if (g.splits == 2) join(std::integral_constant<int, 2>{});
+                else if (g.splits == 4) join(std::integral_constant<int, 4>{});
+                else join(std::integral_constant<int, 8>{});
             }
             __syncwarp();
             cluster_sync_all();
@@ -507,7 +543,7 @@ Plan make_plan(int64_t n_tiles, int64_t M, int kb, int sms, int min_bn, int per_
     for (int bn = min_bn; bn <= 256; bn *= 2) {
         const int64_t tt = (M + bn - 1) / bn, tiles = n_tiles * tt;
         for (int s = 1; s <= 8; s *= 2) {
-            if (s > 1 && (s > kb || tiles * s > sms)) break;
+            if (s > 1 && (2 * s > kb || tiles * s > sms)) break;
             const double per_kb = fmax(bn, (kABytes + bn * 128.0) / 24.0);
             const double waves = s > 1 ? 1.0 : (double)((tiles + sms - 1) / sms);
             const double body = (double)((kb + s - 1) / s) * per_kb;
@@ -525,7 +561,7 @@ Plan make_plan(int64_t n_tiles, int64_t M, int kb, int sms, int min_bn, int per_
     return best;
 }
 
-template <int EPI, typename T, typename O>
+template <int EPI, int LAY, typename T, typename O>
 int launch(const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0, const CUtensorMap& b1, const GemmArgs& g,
            int grid, cudaStream_t stream) {
     const int smem = g.stages * (kABytes + g.bn * kBK * 2) + 1024;
@@ -533,7 +569,7 @@ int launch(const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0, 
     cudaGetDevice(&dev);
     static std::atomic<bool> ready[64];
     if (dev >= 64 || !ready[dev].load()) {
-        cudaError_t e = cudaFuncSetAttribute(gemm_kernel<EPI, T, O>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(gemm_kernel<EPI, LAY, T, O>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              kRingBytes + 1024);
         if (e != cudaSuccess) return op_fail(KD_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
         if (dev < 64) ready[dev].store(true);
@@ -551,7 +587,7 @@ int launch(const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0, 
         cfg.attrs = at;
         cfg.numAttrs = 1;
     }
-    cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_kernel<EPI, T, O>, a0, a1, b0, b1, g);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_kernel<EPI, LAY, T, O>, a0, a1, b0, b1, g);
     if (e != cudaSuccess) return op_fail(KD_ECUDA, "launch failed: %s", cudaGetErrorString(e));
     return KD_OK;
 }
@@ -570,20 +606,18 @@ int run_typed(GemmArgs g, int dtype, const Operand* a, const Operand* b, int pai
     const int per = gated ? 64 : 128;
     const int64_t n_tiles = (g.N + per - 1) / per;
     const int64_t kblocks = (k + kBK - 1) / kBK;
+    const Plan p = make_plan(n_tiles, g.M, (int)kblocks * (gated ? 1 : pairs), sms, b[0].mn ? 64 : 16, (int)sizeof(O));
     g.kb0 = (int)kblocks;
-    g.kb = (int)(kblocks * (gated ? 1 : pairs));
-    const Plan p = make_plan(n_tiles, g.M, g.kb, sms, b[0].mn ? 64 : 16, (int)sizeof(O));
+    g.kb = (int)kblocks * (gated ? 1 : pairs);
     const int64_t t_tiles = (g.M + p.bn - 1) / p.bn;
     if (n_tiles * t_tiles > 0x3fffffff) return op_fail(KD_EINVAL, "too many output tiles");
     g.n_tiles = (int)n_tiles;
     g.t_tiles = (int)t_tiles;
     g.bn = p.bn;
     g.splits = p.splits;
-    g.a_mn = a[0].mn;
-    g.b_mn = b[0].mn;
     g.stages = kRingBytes / (kABytes + p.bn * kBK * 2);
     if (g.stages > kMaxRing) g.stages = kMaxRing;
-    g.idesc = make_idesc(128, p.bn, dtype == KD_BF16, g.a_mn, g.b_mn);
+    g.idesc = make_idesc(128, p.bn, dtype == KD_BF16, a[0].mn, b[0].mn);
     CUtensorMap ma[2], mb[2];
     const int a_box = gated ? 16 : 128;
     if ((rc = operand_map(&ma[0], dtype, a[0], g.N, k, a_box))) return rc;
@@ -594,7 +628,11 @@ int run_typed(GemmArgs g, int dtype, const Operand* a, const Operand* b, int pai
         if ((rc = operand_map(&ma[1], dtype, a[1], g.N, k, a_box))) return rc;
         if (!gated && (rc = operand_map(&mb[1], dtype, b[1], g.M, k, p.bn))) return rc;
     }
-    return launch<EPI, T, O>(ma[0], ma[1], mb[0], mb[1], g, p.grid, stream);
+    if constexpr (EPI == EPI_LINEAR) {
+        if (b[0].mn) return launch<EPI, LAY_MM, T, O>(ma[0], ma[1], mb[0], mb[1], g, p.grid, stream);
+        if (a[0].mn) return launch<EPI, LAY_MK, T, O>(ma[0], ma[1], mb[0], mb[1], g, p.grid, stream);
+    }
+    return launch<EPI, LAY_KK, T, O>(ma[0], ma[1], mb[0], mb[1], g, p.grid, stream);
 }
 
 template <int EPI>

@@ -15,16 +15,20 @@ namespace kd {
 // kd_op_sync reads and clears them.
 static __device__ unsigned int g_op_status;
 
-constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // of every device-side wait
-constexpr unsigned long long kDrainNs = 100000000ull;       // of the wait for copies in flight
+// Limits in SM clocks (about 2 s and 0.1 s at 1.9 GHz). The waits read the SM's own clock: a
+// read of the global timer costs about as much as the wait it would guard.
+constexpr long long kWaitClocks = 4000000000ll;  // of every device-side wait
+constexpr long long kDrainClocks = 200000000ll;  // of the wait for copies in flight
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return (uint32_t)__cvta_generic_to_shared(p);
 }
-__device__ __forceinline__ unsigned long long now_ns() {
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
+// One lane of a fully converged warp. The compiler knows of elect.sync that one lane runs what
+// follows, and then feeds tcgen05 and TMA instructions from uniform registers directly.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n.reg .pred q;\nelect.sync _|q, 0xffffffff;\nselp.b32 %0, 1, 0, q;\n}" : "=r"(p));
+    return p != 0;
 }
 
 // ---------------------------------------------------------------- mbarriers
@@ -45,7 +49,19 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n.reg .pred p;\n"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "selp.b32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// A look that does not wait (try_wait may suspend the thread for a while).
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\n"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
         "selp.b32 %0, 1, 0, p;\n}"
         : "=r"(ok)
         : "r"(bar), "r"(parity)
@@ -54,26 +70,32 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
 }
 // Waits until the phase of `parity` has completed. Gives up when the limit has passed or
 // another wait of this CTA has given up (*dead), and then returns false: the caller unwinds.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* dead,
-                                          unsigned long long limit = kWaitLimitNs) {
-    if (mbar_try(bar, parity)) return true;
-    const unsigned long long t0 = now_ns();
+__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int* dead) {
+    const long long t0 = clock64();
     for (;;) {
         for (int i = 0; i < 32; ++i)
             if (mbar_try(bar, parity)) return true;
         if (*dead) return false;
-        if (now_ns() - t0 > limit) {
+        if (clock64() - t0 > kWaitClocks) {
             *dead = 1;
             atomicExch(&g_op_status, 1u);
             return false;
         }
     }
 }
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
+    if (mbar_try(bar, parity)) return true;
+    return mbar_wait_long(bar, parity, dead);
+}
+// The same by all lanes of a warp, with one answer.
+__device__ __forceinline__ bool mbar_wait_all(uint32_t bar, uint32_t parity, volatile int* dead) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, dead)) != 0;
+}
 // The same, bounded, without the give-up flag: used only to let copies in flight land.
 __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
-    const unsigned long long t0 = now_ns();
+    const long long t0 = clock64();
     while (!mbar_try(bar, parity))
-        if (now_ns() - t0 > kDrainNs) return;
+        if (clock64() - t0 > kDrainClocks) return;
 }
 
 __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
