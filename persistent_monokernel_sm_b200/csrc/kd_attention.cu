@@ -142,21 +142,23 @@ __global__ void __launch_bounds__(kThr, 1)
     if (warp >= 8) {
       set_regs_down<kAuxRegs>();
       if (warp == 8) {  // ---------------------------------------------- producer
-        if (lane == 0) {
+        if (elect_one()) {
             const int two = !a.shared && tile[1] < a.tiles ? 2 : 1;
             mbar_expect(qbar, two * kHalves * a.tq * a.r * 128);
             for (int s = 0; s < two; ++s)
                 for (int h = 0; h < kHalves; ++h)
                     tma_3d(qs + s * kBlock + h * 16384, &mq, h * 64, g * a.r, tile[s] * a.tq, qbar);
-            int it = 0;
+            int it = 0, st = 0;
+            uint32_t ph = 1;
             bool ok = true;
             auto load = [&](const CUtensorMap* m, int block) {
-                const int st = it % kSlots;
-                if (!ok || !(ok = mbar_wait(empty + 8 * st, ((it / kSlots) & 1) ^ 1, dead))) return;
+                if (!ok || !(ok = mbar_wait(empty + 8 * st, ph, dead))) return;
                 mbar_expect(full + 8 * st, kBlock);
+#pragma unroll
                 for (int h = 0; h < kHalves; ++h)
                     tma_3d(ring + st * kBlock + h * 16384, m, h * 64, (lo + block) * kKeys, g, full + 8 * st);
                 ++it;
+                if (++st == kSlots) st = 0, ph ^= 1;
             };
             for (int i = 0; i < ahead; ++i) load(&mk, i);
             for (int i = 0; i < total && ok; ++i) {
@@ -171,7 +173,7 @@ __global__ void __launch_bounds__(kThr, 1)
         }
         __syncwarp();
     } else if (warp == 9) {  // --------------------------------------- issuer
-        if (lane == 0) {
+        if (elect_one()) {
             bool ok = mbar_wait(qbar, 0, dead);
             auto wait_seq = [&](int q) { return ok = ok && mbar_wait(full + 8 * (q % kSlots), (q / kSlots) & 1, dead); };
             auto free_seq = [&](int q) { tc_commit(empty + 8 * (q % kSlots)); };
@@ -263,7 +265,7 @@ __global__ void __launch_bounds__(kThr, 1)
         float m = -INFINITY, l = 0.f;
         bool ok = true;
         for (int i = 0; i < nb[s]; ++i) {
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(sbar + 8 * s, i & 1, dead)))) break;
+            if (!(ok = mbar_wait_all(sbar + 8 * s, i & 1, dead))) break;
             if (any) {
                 tc_fence_after();
                 uint32_t z[kKeys];
@@ -321,9 +323,9 @@ __global__ void __launch_bounds__(kThr, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(pbar + 8 * s);
         }
-        if (ok && nb[s] > 0) ok = __all_sync(0xffffffffu, mbar_wait(obar + 8 * s, 0, dead));
+        if (ok && nb[s] > 0) ok = mbar_wait_all(obar + 8 * s, 0, dead);
         // the partial outputs go where the blocks were: the other stream has to be done too
-        if (ok && a.shared && nb[s ^ 1] > 0) ok = __all_sync(0xffffffffu, mbar_wait(obar + 8 * (s ^ 1), 0, dead));
+        if (ok && a.shared && nb[s ^ 1] > 0) ok = mbar_wait_all(obar + 8 * (s ^ 1), 0, dead);
         tc_fence_after();
         if (!a.shared) {
             if (ok && any && nb[s] > 0) {
