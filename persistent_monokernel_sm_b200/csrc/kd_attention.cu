@@ -65,6 +65,31 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// Two fp32 values in a 64-bit register, and Blackwell's packed arithmetic on them.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pack2(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float lo2(f2 v) {
+    return __uint_as_float((uint32_t)v);
+}
+__device__ __forceinline__ float hi2(f2 v) {
+    return __uint_as_float((uint32_t)(v >> 32));
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 both(float v) { return pack2(v, v); }
+
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
@@ -79,7 +104,7 @@ __global__ void __launch_bounds__(kThr, 1)
                      const __grid_constant__ CUtensorMap mv, const __grid_constant__ AttnArgs a) {
     constexpr int kSlots = Shape<HD>::slots, kBlock = Shape<HD>::block, kPart = Shape<HD>::part, kHalves = HD / 64;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t s_full[kSlots], s_empty[kSlots], s_q, s_s[2], s_p[2], s_o[2], s_drain;
+    __shared__ __align__(8) uint64_t s_full[kSlots], s_empty[kSlots], s_q, s_s[2], s_p[4], s_o[2], s_drain;
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_dead;
 
@@ -115,15 +140,14 @@ __global__ void __launch_bounds__(kThr, 1)
         nb[1] = tile[1] < a.tiles ? blocks_of(tile[1]) : 0;
         total = max(nb[0], nb[1]);
     }
-    // Order of the ring: K_0 (and K_1 with alternate blocks), then V_i, K_(i + ahead) in turn.
+    // Order of the ring: K_0 (and K_1 with alternate blocks), then V_i, K_(i + ahead) in turn;
+    // the issuer uses them in this order.
     const int ahead = min(a.shared ? 2 : 1, total);
-    auto seq_k = [&](int i) { return i < ahead ? i : ahead + 2 * (i - ahead) + 1; };
-    auto seq_v = [&](int i) { return ahead + i + min(i, total - ahead); };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kSlots; ++i) mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, 1);
         mbar_init(qbar, 1);
-        for (int i = 0; i < 2; ++i) mbar_init(sbar + 8 * i, 1), mbar_init(pbar + 8 * i, 4), mbar_init(obar + 8 * i, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(sbar + 8 * i, 1), mbar_init(pbar + 16 * i, 4), mbar_init(pbar + 16 * i + 8, 4), mbar_init(obar + 8 * i, 1);
         mbar_init(drain, 1);
         s_dead = 0;
         fence_barrier_init();
@@ -174,67 +198,83 @@ __global__ void __launch_bounds__(kThr, 1)
         __syncwarp();
     } else if (warp == 9) {  // --------------------------------------- issuer
         if (elect_one()) {
+            // This thread has to keep ahead of two streams' softmax: slots and descriptors are
+            // carried along, and the blocks of an iteration are waited for before its weights.
+            constexpr uint32_t kHop = kBlock >> 4;
+            const uint64_t q_desc = make_desc(qs, 16, 1024), k_desc = make_desc(ring, 16, 1024);
+            const uint64_t v_desc = make_desc(ring, 16384, 1024);
+            const uint32_t idesc_s = a.idesc_s, idesc_o = a.idesc_o;
+            const int n0 = nb[0], n1 = nb[1];
+            int slot = 0;
+            uint32_t ph = 0;
             bool ok = mbar_wait(qbar, 0, dead);
-            auto wait_seq = [&](int q) { return ok = ok && mbar_wait(full + 8 * (q % kSlots), (q / kSlots) & 1, dead); };
-            auto free_seq = [&](int q) { tc_commit(empty + 8 * (q % kSlots)); };
-            auto scores = [&](int s, int q) {  // S_s = Q K^T from slot q
-                const uint32_t ka = ring + (q % kSlots) * kBlock, qa = qs + (a.shared ? 0 : s) * kBlock;
+            auto take = [&]() {  // the next slot of the ring, once it is filled
+                const int at = slot;
+                ok = ok && mbar_wait(full + 8 * at, ph, dead);
+                if (++slot == kSlots) slot = 0, ph ^= 1;
+                return at;
+            };
+            auto scores = [&](int s, int at) {  // S_s = Q K^T
+                const uint64_t kd = k_desc + (uint32_t)at * kHop, qd = q_desc + (a.shared ? 0u : (uint32_t)s * kHop);
 #pragma unroll
                 for (int ks = 0; ks < HD / 16; ++ks) {
-                    const uint32_t off = (ks >> 2) * 16384 + (ks & 3) * 32;
-                    mma_ss<1>(tmem + s * 128, make_desc(qa + off, 16, 1024), make_desc(ka + off, 16, 1024), a.idesc_s, ks > 0);
+                    const uint32_t off = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
+                    mma_ss<1>(tmem + s * 128, qd + off, kd + off, idesc_s, ks > 0);
                 }
                 tc_commit(sbar + 8 * s);
             };
-            auto values = [&](int s, int i, int q) {  // O_s += P_s V from slot q; i: block of the stream
-                if (!(ok = ok && mbar_wait(pbar + 8 * s, i & 1, dead))) return;
-                tc_fence_after();
-                const uint32_t va = ring + (q % kSlots) * kBlock;
+            auto values = [&](int s, int i, int at, bool last) {  // O_s += P_s V; i: block of the stream
+                const uint64_t vd = v_desc + (uint32_t)at * kHop;
 #pragma unroll
-                for (int ks = 0; ks < kKeys / 16; ++ks)
-                    mma_ts(tmem + 256 + s * HD, tmem + s * 128 + ks * 8, make_desc(va + ks * 2048, 16384, 1024), a.idesc_o,
-                           i > 0 || ks > 0);
-                if (i == nb[s] - 1) tc_commit(obar + 8 * s);
-            };
-            tc_fence_after();
-            if (a.shared) {
-                for (int i = 0; i < ahead && wait_seq(i); ++i) {
+                for (int half = 0; half < 2; ++half) {  // as the weights of half a block are there
+                    if (!(ok = ok && mbar_wait(pbar + 16 * s + 8 * half, i & 1, dead))) return;
                     tc_fence_after();
-                    scores(i, i);
-                    free_seq(i);
+#pragma unroll
+                    for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
+                        mma_ts(tmem + 256 + s * HD, tmem + s * 128 + ks * 8, vd + ks * (2048 >> 4), idesc_o, i > 0 || ks > 0);
+                }
+                if (last) tc_commit(obar + 8 * s);
+            };
+            if (a.shared) {
+                for (int i = 0; i < ahead && ok; ++i) {
+                    const int k = take();
+                    if (!ok) break;
+                    tc_fence_after();
+                    scores(i, k);
+                    tc_commit(empty + 8 * k);
                 }
                 for (int i = 0; i < total && ok; ++i) {
-                    const int s = i & 1, v = seq_v(i);
-                    if (!wait_seq(v)) break;
-                    values(s, i >> 1, v);
+                    const int s = i & 1, v = take(), k = i + 2 < total ? take() : -1;
                     if (!ok) break;
-                    free_seq(v);
-                    if (i + 2 < total) {
-                        const int k = seq_k(i + 2);
-                        if (!wait_seq(k)) break;
-                        tc_fence_after();
-                        scores(s, k);
-                        free_seq(k);
-                    }
+                    values(s, i >> 1, v, i + 2 >= total);
+                    if (!ok) break;
+                    if (k >= 0) scores(s, k);
+                    tc_commit(empty + 8 * v);
+                    if (k >= 0) tc_commit(empty + 8 * k);
                 }
-            } else if (wait_seq(0)) {
-                tc_fence_after();
-                scores(0, 0);
-                if (nb[1] > 0) scores(1, 0);
-                free_seq(0);
+            } else {
+                const int first = take();
+                if (ok) {
+                    tc_fence_after();
+                    scores(0, first);
+                    if (n1 > 0) scores(1, first);
+                    tc_commit(empty + 8 * first);
+                }
                 for (int i = 0; i < total && ok; ++i) {
-                    const int v = seq_v(i), k = i + 1 < total ? seq_k(i + 1) : -1;
-                    if (!wait_seq(v)) break;
-                    for (int s = 0; s < 2 && ok; ++s) {
-                        if (i < nb[s]) values(s, i, v);
-                        if (ok && i + 1 < nb[s] && wait_seq(k)) {
-                            tc_fence_after();
-                            scores(s, k);
-                        }
-                    }
+                    const int v = take(), k = i + 1 < total ? take() : -1;
                     if (!ok) break;
-                    free_seq(v);
-                    if (k >= 0) free_seq(k);
+                    if (i < n0) {
+                        values(0, i, v, i == n0 - 1);
+                        if (!ok) break;
+                        if (i + 1 < n0) scores(0, k);
+                    }
+                    if (i < n1) {
+                        values(1, i, v, i == n1 - 1);
+                        if (!ok) break;
+                        if (i + 1 < n1) scores(1, k);
+                    }
+                    tc_commit(empty + 8 * v);
+                    if (k >= 0) tc_commit(empty + 8 * k);
                 }
             }
             if (!ok) {
@@ -302,26 +342,33 @@ __global__ void __launch_bounds__(kThr, 1)
                     }
                 }
                 const float ref = m == -INFINITY ? 0.f : -m;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const f2 scale2 = both(a.scale_log2), ref2 = both(ref);
+                f2 sum[2] = {0ull, 0ull};
 #pragma unroll
-                for (int c = 0; c < kKeys; c += 32) {
-                    uint32_t p[16];
+                for (int half = 0; half < 2; ++half) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float e0 = ex2(fmaf(__uint_as_float(z[c + 2 * j]), a.scale_log2, ref));
-                        const float e1 = ex2(fmaf(__uint_as_float(z[c + 2 * j + 1]), a.scale_log2, ref));
-                        sum[j & 1] += e0;
-                        sum[2 + (j & 1)] += e1;
-                        p[j] = Half2<T>::pack(e0, e1);
+                    for (int c = 64 * half; c < 64 * half + 64; c += 32) {
+                        uint32_t p[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const f2 x = fma2(pack2(__uint_as_float(z[c + 2 * j]), __uint_as_float(z[c + 2 * j + 1])), scale2, ref2);
+                            const f2 e = pack2(ex2(lo2(x)), ex2(hi2(x)));
+                            sum[j & 1] = add2(sum[j & 1], e);
+                            p[j] = Half2<T>::pack(lo2(e), hi2(e));
+                        }
+                        tmem_st16(S + c / 2, p);
                     }
-                    tmem_st16(S + c / 2, p);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(pbar + 16 * s + 8 * half);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                tmem_wait_st();
-                tc_fence_before();
+                const f2 all = add2(sum[0], sum[1]);
+                l += lo2(all) + hi2(all);
+            } else if (lane == 0) {
+                mbar_arrive(pbar + 16 * s);
+                mbar_arrive(pbar + 16 * s + 8);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(pbar + 8 * s);
         }
         if (ok && nb[s] > 0) ok = mbar_wait_all(obar + 8 * s, 0, dead);
         // the partial outputs go where the blocks were: the other stream has to be done too
