@@ -17,7 +17,8 @@ __all__ = ["KdError", "kd_config", "kd_weights", "kd_info", "load_library", "Dec
            "kd_decode", "kd_generate", "kd_sync", "kd_position", "kd_set_trace", "kd_set_timeout", "kd_set_sampling", "kd_decode_noalloc", "kd_get_info", "kd_kv_ptr",
            "kd_last_error", "kd_strerror", "kd_destroy", "LIB_PATH", "ERRORS",
            "kd_linear_args", "kd_gated_args", "kd_linear", "kd_gated_ffn", "kd_gated_ffn_backward_workspace",
-           "kd_gated_ffn_backward", "kd_attention_args", "kd_prompt_attention", "kd_op_sync", "kd_op_error",
+           "kd_gated_ffn_backward", "kd_attention_args", "kd_prompt_attention_workspace",
+           "kd_prompt_attention", "kd_op_sync", "kd_op_error",
            "kd_prefill_workspace", "kd_prefill",
            "linear", "gated_ffn", "gated_ffn_backward", "prompt_attention"]
 
@@ -84,7 +85,7 @@ class kd_attention_args(ctypes.Structure):
                 ("k", ctypes.c_void_p), ("k_pos", ctypes.c_int64), ("k_head", ctypes.c_int64),
                 ("v", ctypes.c_void_p), ("v_pos", ctypes.c_int64), ("v_head", ctypes.c_int64),
                 ("out", ctypes.c_void_p), ("out_token", ctypes.c_int64), ("out_head", ctypes.c_int64),
-                ("scale", ctypes.c_float)]
+                ("scale", ctypes.c_float), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
 class KdError(RuntimeError):
@@ -134,6 +135,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "kd_gated_ffn": (ctypes.c_int, [ctypes.c_char_p, _P, ctypes.c_int64, _P]),
         "kd_gated_ffn_backward_workspace": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64]),
         "kd_gated_ffn_backward": (ctypes.c_int, [ctypes.c_char_p] + [_P, ctypes.c_int64] * 4 + [_P, ctypes.c_size_t, _P]),
+        "kd_prompt_attention_workspace": (ctypes.c_size_t, [ctypes.c_char_p]),
         "kd_prompt_attention": (ctypes.c_int, [ctypes.c_char_p, _P]),
         "kd_op_sync": (ctypes.c_int, [_P]),
         "kd_op_error": (ctypes.c_char_p, []),
@@ -273,6 +275,10 @@ def kd_gated_ffn_backward(args: kd_gated_args, dh: int, ld_dh: int, dx: int | No
                           stream: int | None) -> int:
     return _check_op(load_library().kd_gated_ffn_backward(bytes(args), dh, ld_dh, dx, ld_dx, dwg, ld_dwg, dwu, ld_dwu,
                                                           workspace, workspace_bytes, stream), "kd_gated_ffn_backward")
+
+
+def kd_prompt_attention_workspace(args: kd_attention_args) -> int:
+    return load_library().kd_prompt_attention_workspace(bytes(args))
 
 
 def kd_prompt_attention(args: kd_attention_args, stream: int | None) -> int:

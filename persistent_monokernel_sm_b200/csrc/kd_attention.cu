@@ -43,7 +43,8 @@ struct AttnArgs {
     int n, kv_len, r, hkv;
     int tq;      // tokens per tile
     int tiles;   // query tiles
-    int splits;  // CTAs per cluster
+    int splits;  // CTAs that share the blocks of a tile (and of a kv head)
+    float* parts;  // their partial outputs: [CTA][row][HD outputs, m, l, 2 unused]
     int shared;  // the streams share a tile (alternate blocks)
     uint32_t idesc_s, idesc_o;
     float scale_log2;
@@ -90,6 +91,23 @@ __device__ __forceinline__ f2 add2(f2 a, f2 b) {
 }
 __device__ __forceinline__ f2 both(float v) { return pack2(v, v); }
 
+// HD / 32 neighbouring outputs of a row, from one lane.
+template <int HD, typename T>
+__device__ __forceinline__ void store_row(const AttnArgs& a, int tok, int head, int lane, const float* o, float inv) {
+    constexpr int E = HD / 32;
+    T* out = (T*)a.out + (int64_t)tok * a.out_token + (int64_t)head * a.out_head + lane * E;
+    uint32_t w[E / 2];
+#pragma unroll
+    for (int e = 0; e < E; e += 2) w[e / 2] = Half2<T>::pack(o[e] * inv, o[e + 1] * inv);
+    if constexpr (E == 4) *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(out) = w[0];
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
@@ -116,11 +134,12 @@ __global__ void __launch_bounds__(kThr, 1)
     volatile int* dead = &s_dead;
     // (m, l) of the two streams' rows for the join: where a second query tile would be
     float* stat = reinterpret_cast<float*>(smem_raw + (qs + kBlock - smem_u32(smem_raw)));
-    const uint32_t stat_at = qs + kBlock;
+    auto part_at = [&](int s, int row) {  // a row's partial output, where the blocks were
+        return reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw))) + (s * 128 + row) * kPart;
+    };
 
     // What this CTA works on: a kv head, one or two tiles, a range of blocks per stream.
-    const int rank = a.splits > 1 ? (int)cluster_rank() : 0;
-    const int unit = blockIdx.x / a.splits;
+    const int rank = blockIdx.x % a.splits, unit = blockIdx.x / a.splits;
     const int g = unit % a.hkv;
     int tile[2], nb[2], lo = 0, total;  // nb: blocks of each stream; total: blocks streamed
     auto blocks_of = [&](int t) {
@@ -226,11 +245,11 @@ __global__ void __launch_bounds__(kThr, 1)
             auto values = [&](int s, int i, int at, bool last) {  // O_s += P_s V; i: block of the stream
                 const uint64_t vd = v_desc + (uint32_t)at * kHop;
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {  // as the weights of half a block are there
-                    if (!(ok = ok && mbar_wait(pbar + 16 * s + 8 * half, i & 1, dead))) return;
+                for (int part = 0; part < 2; ++part) {  // as the weights of three quarters, of all are there
+                    if (!(ok = ok && mbar_wait(pbar + 16 * s + 8 * part, i & 1, dead))) return;
                     tc_fence_after();
 #pragma unroll
-                    for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
+                    for (int ks = 6 * part; ks < 6 + 2 * part; ++ks)
                         mma_ts(tmem + 256 + s * HD, tmem + s * 128 + ks * 8, vd + ks * (2048 >> 4), idesc_o, i > 0 || ks > 0);
                 }
                 if (last) tc_commit(obar + 8 * s);
@@ -284,15 +303,7 @@ __global__ void __launch_bounds__(kThr, 1)
         }
         __syncwarp();
       }
-      if (a.shared) {  // the join's meetings
-          __syncwarp();
-          if (a.splits > 1) {
-              cluster_sync_all();
-              cluster_sync_all();
-          } else {
-              __syncthreads();
-          }
-      }
+      if (a.shared) __syncthreads();  // the streams' join
     } else {  // ------------------------------------------------------ softmax
         set_regs_up<kRowRegs>();
         const int s = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
@@ -309,19 +320,27 @@ __global__ void __launch_bounds__(kThr, 1)
             if (any) {
                 tc_fence_after();
                 uint32_t z[kKeys];
-#pragma unroll
-                for (int c = 0; c < kKeys; c += 32) tmem_ld32(S + c, z + c);
-                tmem_wait_ld();
                 const int left = seen - (lo + (a.shared ? 2 * i + s : i)) * kKeys;  // keys of this block it sees
-                if (__any_sync(0xffffffffu, left < kKeys)) {
-#pragma unroll
-                    for (int c = 0; c < kKeys; ++c)
-                        if (c >= left) z[c] = 0xff800000u;
-                }
+                const bool cut = __any_sync(0xffffffffu, left < kKeys);
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                tmem_ld32(S, z);
+                tmem_ld32(S + 32, z + 32);
+                tmem_wait_ld();
+                tmem_ld32(S + 64, z + 64);
+                tmem_ld32(S + 96, z + 96);
 #pragma unroll
-                for (int c = 0; c < kKeys; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(z[c]));
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+                for (int half = 0; half < 2; ++half) {
+                    if (half) tmem_wait_ld();
+                    if (cut) {
+#pragma unroll
+                        for (int c = 64 * half; c < 64 * half + 64; ++c)
+                            if (c >= left) z[c] = 0xff800000u;
+                    }
+#pragma unroll
+                    for (int c = 64 * half; c < 64 * half + 64; c += 2)
+                        mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], __uint_as_float(z[c]), __uint_as_float(z[c + 1]));
+                }
+                const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * a.scale_log2;
                 // m is the reference in log2 units; -inf while the row has seen nothing
                 const bool grow = top > m + kLazy || (m == -INFINITY && top > -INFINITY);
                 if (__any_sync(0xffffffffu, grow)) {
@@ -345,9 +364,9 @@ __global__ void __launch_bounds__(kThr, 1)
                 const f2 scale2 = both(a.scale_log2), ref2 = both(ref);
                 f2 sum[2] = {0ull, 0ull};
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
+                for (int part = 0; part < 2; ++part) {  // three quarters, then the last
 #pragma unroll
-                    for (int c = 64 * half; c < 64 * half + 64; c += 32) {
+                    for (int c = 96 * part; c < 96 + 32 * part; c += 32) {
                         uint32_t p[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
@@ -361,7 +380,7 @@ __global__ void __launch_bounds__(kThr, 1)
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(pbar + 16 * s + 8 * half);
+                    if (lane == 0) mbar_arrive(pbar + 16 * s + 8 * part);
                 }
                 const f2 all = add2(sum[0], sum[1]);
                 l += lo2(all) + hi2(all);
@@ -395,11 +414,11 @@ __global__ void __launch_bounds__(kThr, 1)
                     }
                 }
             }
-        } else {  // leave (m, l, o) for the join; the ring is free: every copy has been used
+        } else {  // leave (m, l, o) for the join below; the ring is free: every copy has been used
             stat[s * 256 + row] = m;
             stat[s * 256 + 128 + row] = l;
             if (ok && any && nb[s] > 0) {
-                float* part = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw))) + (s * 128 + row) * kPart;
+                float* part = part_at(s, row);
 #pragma unroll
                 for (int c = 0; c < HD; c += 32) {
                     uint32_t o[32];
@@ -412,38 +431,40 @@ __global__ void __launch_bounds__(kThr, 1)
         }
         tc_fence_before();
         if (a.shared) {
-            // join: a warp per row; lane holds HD / 32 neighbouring outputs
-            __syncwarp();
-            if (a.splits > 1) cluster_sync_all();
-            else __syncthreads();
+            // The two streams' partials of a row are joined by a warp, whose lanes hold HD / 32
+            // neighbouring outputs each; a split tile's go to the workspace for join_kernel.
+            __syncthreads();
             if (!*dead) {
                 const int tokens = min(a.tq, a.n - tile[0] * a.tq), rows = tokens * a.r;
                 constexpr int E = HD / 32;
-                for (int row = rank * 8 + warp; row < rows; row += 8 * a.splits) {
-                    float best = -INFINITY;
-                    for (int p = 0; p < 2 * a.splits; ++p)
-                        best = fmaxf(best, ld_cluster_f32(map_rank(stat_at + ((p & 1) * 256 + row) * 4, p >> 1)));
+                for (int row = warp; row < rows; row += 8) {
+                    const float m0 = stat[row], m1 = stat[256 + row], best = fmaxf(m0, m1);
+                    // a stream that saw nothing wrote no output
+                    const float w0 = m0 == -INFINITY ? 0.f : ex2(m0 - best), w1 = m1 == -INFINITY ? 0.f : ex2(m1 - best);
                     float l = 0.f, o[E];
-    #pragma unroll
+                    const float *p0 = part_at(0, row) + lane * E, *p1 = part_at(1, row) + lane * E;
+#pragma unroll
                     for (int e = 0; e < E; ++e) o[e] = 0.f;
-                    for (int p = 0; p < 2 * a.splits; ++p) {
-                        const float m = ld_cluster_f32(map_rank(stat_at + ((p & 1) * 256 + row) * 4, p >> 1));
-                        if (m == -INFINITY) continue;  // saw nothing: its output was never written
-                        const float w = ex2(m - best);
-                        l += w * ld_cluster_f32(map_rank(stat_at + ((p & 1) * 256 + 128 + row) * 4, p >> 1));
-                        const uint32_t src = map_rank(ring + (((p & 1) * 128 + row) * kPart + lane * E) * 4, p >> 1);
-    #pragma unroll
-                        for (int e = 0; e < E; ++e) o[e] += w * ld_cluster_f32(src + 4 * e);
+                    if (m0 != -INFINITY) {
+                        l = w0 * stat[128 + row];
+#pragma unroll
+                        for (int e = 0; e < E; ++e) o[e] = w0 * p0[e];
                     }
-                    const float inv = 1.f / l;
-                    T* out = (T*)a.out + (int64_t)(tile[0] * a.tq + row / a.r) * a.out_token +
-                             (int64_t)(g * a.r + row % a.r) * a.out_head + lane * E;
-    #pragma unroll
-                    for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(out + e) = Half2<T>::pack(o[e] * inv, o[e + 1] * inv);
+                    if (m1 != -INFINITY) {
+                        l += w1 * stat[384 + row];
+#pragma unroll
+                        for (int e = 0; e < E; ++e) o[e] = fmaf(w1, p1[e], o[e]);
+                    }
+                    if (a.splits == 1) {
+                        store_row<HD, T>(a, tile[0] * a.tq + row / a.r, g * a.r + row % a.r, lane, o, 1.f / l);
+                    } else {
+                        float* to = a.parts + ((int64_t)blockIdx.x * 128 + row) * kPart;
+#pragma unroll
+                        for (int e = 0; e < E; ++e) to[lane * E + e] = o[e];
+                        if (lane == 0) to[HD] = best, to[HD + 1] = l;
+                    }
                 }
             }
-            __syncwarp();
-            if (a.splits > 1) cluster_sync_all();
         }
     }
     tc_fence_before();
@@ -452,33 +473,103 @@ __global__ void __launch_bounds__(kThr, 1)
     if (warp == 9) tmem_free<1>(tmem, 512);
 }
 
+// Joins the partial rows of split tiles: a warp per row, which reads eight partials at a time.
+// With m the maximum over the partials that saw anything, o = sum 2^(m_p - m) o_p / sum
+// 2^(m_p - m) l_p, in the order of p.
+template <int HD, typename T>
+__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttnArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int E = HD / 32, kPart = Shape<HD>::part;
+    const int lane = threadIdx.x & 31, per = a.tq * a.r;
+    const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int unit = (int)(w / per), row = (int)(w % per);
+    const int tile = a.tiles - 1 - unit / a.hkv, g = unit % a.hkv, tok = tile * a.tq + row / a.r;
+    if (unit >= a.tiles * a.hkv || tok >= a.n) return;
+    const float* from = a.parts + ((int64_t)unit * a.splits * 128 + row) * kPart;
+    float best = -INFINITY;
+    for (int p = lane; p < a.splits; p += 32) best = fmaxf(best, from[(int64_t)p * 128 * kPart + HD]);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, x));
+    float l = 0.f, o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+    for (int p0 = 0; p0 < a.splits; p0 += 8) {
+        float v[8][E], m[8], s[8];
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+            const float* at = from + (int64_t)min(p0 + p, a.splits - 1) * 128 * kPart;
+            m[p] = at[HD], s[p] = at[HD + 1];
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[p][e] = at[lane * E + e];
+        }
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+            if (p0 + p >= a.splits || m[p] == -INFINITY) continue;
+            const float wp = ex2(m[p] - best);
+            l = fmaf(wp, s[p], l);
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = fmaf(wp, v[p][e], o[e]);
+        }
+    }
+    store_row<HD, T>(a, tok, g * a.r + row % a.r, lane, o, 1.f / l);
+}
+
 template <int HD, typename T>
 int launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const AttnArgs& a, int grid, cudaStream_t s) {
-    constexpr int smem = Shape<HD>::smem;
     static std::atomic<bool> ready[64];
     int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev >= 64 || !ready[dev].load()) {
-        cudaError_t e = cudaFuncSetAttribute(attention_kernel<HD, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return op_fail(KD_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-        if (dev < 64) ready[dev].store(true);
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && (dev >= 64 || !ready[dev].load())) {
+        e = cudaFuncSetAttribute(attention_kernel<HD, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<HD>::smem);
+        if (e == cudaSuccess && dev < 64) ready[dev].store(true);
     }
+    if (e != cudaSuccess) return op_fail(KD_ECUDA, "kd_prompt_attention: %s", cudaGetErrorString(e));
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kThr);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = Shape<HD>::smem;
     cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    if (a.splits > 1) {
-        at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = a.splits;
-        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    e = cudaLaunchKernelEx(&cfg, attention_kernel<HD, T>, q, k, v, a);
+    if (e == cudaSuccess && a.splits > 1) {
+        const int64_t rows = (int64_t)a.tiles * a.hkv * a.tq * a.r;
+        cfg.gridDim = dim3((unsigned)((rows + 3) / 4));
+        cfg.blockDim = dim3(128);
+        cfg.dynamicSmemBytes = 0;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = at;
         cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, join_kernel<HD, T>, a);
     }
-    cudaError_t e = cudaLaunchKernelEx(&cfg, attention_kernel<HD, T>, q, k, v, a);
     if (e != cudaSuccess) return op_fail(KD_ECUDA, "launch failed: %s", cudaGetErrorString(e));
     return KD_OK;
+}
+
+// How the work is cut: the CTAs, whether two streams share a tile, and the split of its blocks.
+// It goes by the sizes and kCtas (the SMs of a B200) alone, so that a workspace can be sized
+// without a device.
+constexpr int kCtas = 148;
+struct Cut {
+    int shared, splits;
+    int64_t grid, bytes;
+};
+Cut cut_of(int64_t n, int64_t kv_len, int r, int hkv, int hd) {
+    const int tq = 128 / r;
+    const int64_t tiles = (n + tq - 1) / tq, units = tiles * hkv, pairs = (tiles + 1) / 2 * hkv;
+    const int64_t blocks = (kv_len + n + kKeys - 1) / kKeys;
+    Cut c{0, 1, pairs, 0};
+    if (units <= kCtas) {
+        // One tile per CTA, and its blocks over as many CTAs as there are SMs while each keeps
+        // two blocks for either stream (one: the join then costs more than it saves).
+        c.shared = 1;
+        const int64_t most = kCtas / units, worth = blocks / 4;
+        c.splits = (int)(most < worth ? most : worth);
+        if (c.splits < 1) c.splits = 1;
+        c.grid = units * c.splits;
+        if (c.splits > 1) c.bytes = c.grid * 128 * (hd + 4) * 4 + 256;
+    }
+    return c;
 }
 
 }  // namespace
@@ -498,9 +589,7 @@ int attention_status(cudaStream_t s, unsigned int* st) {
 
 using namespace kd;
 
-extern "C" int kd_prompt_attention(const kd_attention_args* p, void* stream) {
-    if (!p) return op_fail(KD_EINVAL, "kd_prompt_attention: NULL arguments");
-    kd_attention_args q = *p;
+static int check_attention(const kd_attention_args& q) {
     if (q.dtype != KD_BF16 && q.dtype != KD_F16)
         return op_fail(KD_EINVAL, "kd_prompt_attention: dtype must be KD_BF16 or KD_F16");
     if (q.head_dim != 64 && q.head_dim != 128) return op_fail(KD_EINVAL, "kd_prompt_attention: head_dim must be 64 or 128");
@@ -510,6 +599,19 @@ extern "C" int kd_prompt_attention(const kd_attention_args* p, void* stream) {
     if (q.n < 0 || q.kv_len < 0 || q.n > (1 << 30) || q.kv_len > (1 << 30) - q.n)
         return op_fail(KD_EINVAL, "kd_prompt_attention: n=%lld kv_len=%lld out of range", (long long)q.n, (long long)q.kv_len);
     if (!(q.scale > 0.f) || !(q.scale < INFINITY)) return op_fail(KD_EINVAL, "kd_prompt_attention: scale must be finite and > 0");
+    return KD_OK;
+}
+
+extern "C" size_t kd_prompt_attention_workspace(const kd_attention_args* p) {
+    if (!p || check_attention(*p) || p->n == 0) return 0;
+    return (size_t)cut_of(p->n, p->kv_len, p->n_heads / p->n_kv_heads, p->n_kv_heads, p->head_dim).bytes;
+}
+
+extern "C" int kd_prompt_attention(const kd_attention_args* p, void* stream) {
+    if (!p) return op_fail(KD_EINVAL, "kd_prompt_attention: NULL arguments");
+    kd_attention_args q = *p;
+    int rc = check_attention(q);
+    if (rc) return rc;
     if (q.n == 0) return KD_OK;
     // the stride of a dimension of one entry is not used
     if (q.n_heads == 1) q.q_head = q.out_head = q.head_dim;
@@ -526,9 +628,6 @@ extern "C" int kd_prompt_attention(const kd_attention_args* p, void* stream) {
             if (st[2 * i + j] < q.head_dim || st[2 * i + j] % 8 || st[2 * i + j] >= (int64_t)1 << 38)
                 return op_fail(KD_EINVAL, "kd_prompt_attention: %s: strides must be multiples of 8, at least head_dim", names[i]);
     }
-    int sms = 0;
-    int rc = op_sm_count(&sms);
-    if (rc) return rc;
     AttnArgs a{};
     a.n = (int)q.n, a.kv_len = (int)q.kv_len;
     a.hkv = q.n_kv_heads, a.r = q.n_heads / q.n_kv_heads;
@@ -536,27 +635,22 @@ extern "C" int kd_prompt_attention(const kd_attention_args* p, void* stream) {
     a.tiles = (a.n + a.tq - 1) / a.tq;
     a.scale_log2 = q.scale * 1.4426950408889634f;
     a.out = q.out, a.out_token = q.out_token, a.out_head = q.out_head;
-    const int64_t T = q.kv_len + q.n, units = (int64_t)a.tiles * a.hkv;
-    const int64_t blocks = (T + kKeys - 1) / kKeys;
-    if (units > 0x3fffffff) return op_fail(KD_EINVAL, "kd_prompt_attention: too many tiles");
-    // Few tiles: one tile per CTA, its blocks split over its two streams and over a cluster of
-    // CTAs as long as the SMs last and a CTA keeps two blocks.
-    int64_t grid;
-    a.splits = 1;
-    if (units <= sms) {
-        a.shared = 1;
-        while (a.splits < 8 && units * a.splits * 2 <= sms && blocks >= a.splits * 4) a.splits *= 2;
-        grid = units * a.splits;
-    } else {
-        grid = (int64_t)((a.tiles + 1) / 2) * a.hkv;
-    }
+    const int64_t T = q.kv_len + q.n;
+    const Cut c = cut_of(q.n, q.kv_len, a.r, a.hkv, q.head_dim);
+    if ((int64_t)a.tiles * a.hkv > 0x3fffffff) return op_fail(KD_EINVAL, "kd_prompt_attention: too many tiles");
+    if (c.bytes > 0 && (!q.workspace || q.workspace_bytes < (size_t)c.bytes))
+        return op_fail(KD_ENOMEM, "kd_prompt_attention: workspace of %zu bytes, need %zu", q.workspace ? q.workspace_bytes : 0,
+                       (size_t)c.bytes);
+    a.shared = c.shared, a.splits = c.splits;
+    a.parts = (float*)(((uintptr_t)q.workspace + 255) & ~(uintptr_t)255);
+    const int64_t grid = c.grid;
+    const bool bf = q.dtype == KD_BF16;
     CUtensorMap mq, mk, mv;
     // Rows past the last position read as zeros (not what the cache holds there): a weight of 0
     // times it is then 0.
     if ((rc = make_map_3d(&mq, q.dtype, q.q, q.head_dim, q.n_heads, q.n, q.q_head, q.q_token, 64, a.r, a.tq))) return rc;
     if ((rc = make_map_3d(&mk, q.dtype, q.k, q.head_dim, T, a.hkv, q.k_pos, q.k_head, 64, kKeys, 1))) return rc;
     if ((rc = make_map_3d(&mv, q.dtype, q.v, q.head_dim, T, a.hkv, q.v_pos, q.v_head, 64, kKeys, 1))) return rc;
-    const bool bf = q.dtype == KD_BF16;
     a.idesc_s = make_idesc(128, kKeys, bf, false, false);
     a.idesc_o = make_idesc(128, q.head_dim, bf, false, true);
     cudaStream_t s = (cudaStream_t)stream;

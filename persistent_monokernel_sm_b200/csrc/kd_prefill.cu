@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(256)
 // The workspace of c tokens: the residual, and one region that holds in turn the Q/K/V outputs
 // and q, then the hidden units; normalised activations and attention outputs share another.
 struct Space {
-    size_t x, xn, qkv, q, att, h, total;
+    size_t x, xn, qkv, q, att, h, part, total;
 };
 size_t up(size_t v) { return (v + 255) & ~(size_t)255; }
 int64_t hidden_ld(int F) { return (F + 7) & ~7; }
@@ -130,7 +130,9 @@ Space space_of(const Dims& d, int64_t c) {
     const size_t qkv_q = s.q + up((size_t)c * d.qd * 2) - s.qkv;
     s.h = s.qkv;
     const size_t h = up((size_t)c * hidden_ld(d.F) * 2);
-    s.total = s.qkv + (qkv_q > h ? qkv_q : h);
+    s.part = s.qkv + (qkv_q > h ? qkv_q : h);
+    // attention's partial results, whatever the size of a piece (the last may be small)
+    s.total = s.part + kAttnPartBytes;
     return s;
 }
 
@@ -221,6 +223,7 @@ int kd_prefill(kd_ctx* c, const int32_t* d_tokens, int32_t n_tokens, int32_t kv_
             t.k = kc, t.v = vc, t.k_pos = t.v_pos = d.hd, t.k_head = t.v_head = (int64_t)d.S * d.hd;
             t.out = att, t.out_token = d.qd, t.out_head = d.hd;
             t.scale = 1.f / sqrtf((float)d.hd);
+            t.workspace = base + sp.part, t.workspace_bytes = sp.total - sp.part;
             if ((rc = op(kd_prompt_attention(&t, s)))) return rc;
             a = kd_linear_args{};  // x += att wo^T
             a.dtype = KD_BF16, a.out_dtype = KD_F32, a.w_transposed = 1;

@@ -23,7 +23,8 @@ _ACT = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3}
 # the C structs of kd.h, field by field
 _LINEAR = struct.Struct("@4i3qPqPqPPqPq")
 _GATED = struct.Struct("@2i3qPqPqPq")
-_ATTENTION = struct.Struct("@4i2q" + "P2q" * 4 + "fi")
+_ATTENTION = struct.Struct("@4i2q" + "P2q" * 4 + "fPN")
+_FEW_ROWS = 128 * 148  # query rows (tokens x heads) above which attention needs no workspace
 _EINVAL = -1
 # The current device and its current stream as plain numbers: the public calls build objects, which
 # costs a call of a few microseconds a fifth of its time.
@@ -196,7 +197,14 @@ def prompt_attention(q, k, v, kv_len, scale=None, out=None):
     qs, ks, vs, os = q.stride(), k.stride(), v.stride(), out.stride()
     if qs[2] != 1 or ks[2] != 1 or vs[2] != 1 or os[2] != 1:
         _refuse("the last dimension must be contiguous")
-    _enqueue(dev, _lib().kd_prompt_attention,
-             _ATTENTION.pack(_DTYPE[dtype], hq, k.shape[0], hd, n, kv_len, q.data_ptr(), qs[0], qs[1], k.data_ptr(),
-                             ks[1], ks[0], v.data_ptr(), vs[1], vs[0], out.data_ptr(), os[0], os[1], scale, 0))
+    lib = _lib()
+    args = (_DTYPE[dtype], hq, k.shape[0], hd, n, kv_len, q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[1], ks[0],
+            v.data_ptr(), vs[1], vs[0], out.data_ptr(), os[0], os[1], scale)
+    size, ws = 0, 0
+    if n * hq <= _FEW_ROWS:  # only few tiles are split
+        size = lib.kd_prompt_attention_workspace(_ATTENTION.pack(*args, 0, 0))
+        if size:
+            buf = _empty(q, (size,), torch.uint8)  # returned to the allocator in stream order
+            ws = buf.data_ptr()
+    _enqueue(dev, lib.kd_prompt_attention, _ATTENTION.pack(*args, ws, size))
     return out
