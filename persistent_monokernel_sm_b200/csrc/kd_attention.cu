@@ -180,6 +180,8 @@ __global__ void __launch_bounds__(kThr, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    grid_wait();
+    grid_release();
     const uint32_t tmem = s_tmem;  // columns: S0, S1 (128 each), O0, O1 (HD each)
 
     if (warp >= 8) {
@@ -478,7 +480,7 @@ __global__ void __launch_bounds__(kThr, 1)
 // 2^(m_p - m) l_p, in the order of p.
 template <int HD, typename T>
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttnArgs a) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_wait();
     constexpr int E = HD / 32, kPart = Shape<HD>::part;
     const int lane = threadIdx.x & 31, per = a.tq * a.r;
     const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
@@ -529,17 +531,17 @@ int launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, con
     cfg.blockDim = dim3(kThr);
     cfg.dynamicSmemBytes = Shape<HD>::smem;
     cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, attention_kernel<HD, T>, q, k, v, a);
     if (e == cudaSuccess && a.splits > 1) {
         const int64_t rows = (int64_t)a.tiles * a.hkv * a.tq * a.r;
         cfg.gridDim = dim3((unsigned)((rows + 3) / 4));
         cfg.blockDim = dim3(128);
         cfg.dynamicSmemBytes = 0;
-        cudaLaunchAttribute at[1];
-        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = at;
-        cfg.numAttrs = 1;
         e = cudaLaunchKernelEx(&cfg, join_kernel<HD, T>, a);
     }
     if (e != cudaSuccess) return op_fail(KD_ECUDA, "launch failed: %s", cudaGetErrorString(e));

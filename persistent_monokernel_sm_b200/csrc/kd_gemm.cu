@@ -278,6 +278,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     tc_fence_after();
     const uint32_t tmem = s_tmem;
     volatile int* dead = &s_dead;
+    // What came before on the stream may still run until here; the next launch may start its own
+    // set-up as this one's CTAs end.
+    grid_wait();
+    grid_release();
 
     const int rank = g.splits > 1 ? (int)cluster_rank() : 0;
     const int first = blockIdx.x / g.splits, step = gridDim.x / g.splits;
@@ -529,26 +533,30 @@ struct Operand {
     bool mn;     // rows run over k (the M or N index is the contiguous one)
 };
 
-// Tile width (tokens) and split of the reduction, by an estimate of the time in SM clocks: a
-// k-block costs what its product takes (16 columns x 128 rows x 64 deep in 16 clocks) or what
-// its bytes take at an SM's share of HBM (24 bytes a clock), whichever is more; a tile costs
-// its start and end besides, and a split the exchange through shared memory.
+// Tile width (tokens) and split of the reduction, by an estimate of the time in microseconds.
+// A k-block costs an SM what its instructions or its product take (measured from one-tile
+// runs: 0.20 us up to 64 columns, 0.28 at 128, 0.41 at 256), or what the CTAs' loads take at the
+// 10.5 TB/s that L2 was seen to deliver to such tiles, whichever is more; a tile's epilogue runs
+// beside the next tile's products; a split costs its exchange. Both sides, measured (us):
+// 128 x 4,096 x 2,048: 32 columns 14.1, 128 columns split by four 15.5; 128 x 1,536 x 4,096: 16
+// columns 17.8, 128 split by eight 11.2; 1,024 x 2,048 x 2,048: 128 columns 13.6, 256 19.4.
 struct Plan {
     int bn, splits, grid;
 };
 
-Plan make_plan(int64_t n_tiles, int64_t M, int kb, int sms, int min_bn, int per_tile_bytes) {
+Plan make_plan(int64_t n_tiles, int64_t M, int kb, int sms, int min_bn) {
     Plan best{};
     double best_cost = 1e300;
     for (int bn = min_bn; bn <= 256; bn *= 2) {
-        const int64_t tt = (M + bn - 1) / bn, tiles = n_tiles * tt;
+        const int64_t tiles = n_tiles * ((M + bn - 1) / bn);
         for (int s = 1; s <= 8; s *= 2) {
             if (s > 1 && (2 * s > kb || tiles * s > sms)) break;
-            const double per_kb = fmax(bn, (kABytes + bn * 128.0) / 24.0);
-            const double waves = s > 1 ? 1.0 : (double)((tiles + sms - 1) / sms);
-            const double body = (double)((kb + s - 1) / s) * per_kb;
-            const double tail = 600.0 + per_tile_bytes * bn * 4.0 + (s > 1 ? 1200.0 + 128.0 * 4.0 * bn / 16.0 : 0.0);
-            const double cost = waves * fmax(body, s > 1 ? 0.0 : tail) + tail + 1500.0;
+            const double work = bn <= 64 ? 0.20 + bn * 0.0003 : bn == 128 ? 0.28 : 0.41;
+            const double ctas = (double)(tiles * s < sms ? tiles * s : sms);
+            const double load = ctas * (kABytes + 128.0 * bn) / 10.5e6;
+            const double body = (double)((kb + s - 1) / s) * (work > load ? work : load), tail = 0.4 + 0.012 * bn;
+            const double waves = (double)((tiles * s + sms - 1) / sms);
+            const double cost = s > 1 ? body + tail / s + 2.0 + 0.025 * bn : waves * (body > tail ? body : tail) + tail;
             if (cost < best_cost) {
                 best_cost = cost;
                 best.bn = bn;
@@ -579,14 +587,14 @@ int launch(const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0, 
     cfg.blockDim = dim3(kGemmThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute at[1];
-    if (g.splits > 1) {
-        at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = g.splits;
-        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-        cfg.attrs = at;
-        cfg.numAttrs = 1;
-    }
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = g.splits;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = g.splits > 1 ? 2 : 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_kernel<EPI, LAY, T, O>, a0, a1, b0, b1, g);
     if (e != cudaSuccess) return op_fail(KD_ECUDA, "launch failed: %s", cudaGetErrorString(e));
     return KD_OK;
@@ -606,7 +614,7 @@ int run_typed(GemmArgs g, int dtype, const Operand* a, const Operand* b, int pai
     const int per = gated ? 64 : 128;
     const int64_t n_tiles = (g.N + per - 1) / per;
     const int64_t kblocks = (k + kBK - 1) / kBK;
-    const Plan p = make_plan(n_tiles, g.M, (int)kblocks * (gated ? 1 : pairs), sms, b[0].mn ? 64 : 16, (int)sizeof(O));
+    const Plan p = make_plan(n_tiles, g.M, (int)kblocks * (gated ? 1 : pairs), sms, b[0].mn ? 64 : 16);
     g.kb0 = (int)kblocks;
     g.kb = (int)kblocks * (gated ? 1 : pairs);
     const int64_t t_tiles = (g.M + p.bn - 1) / p.bn;

@@ -98,6 +98,12 @@ __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
         if (clock64() - t0 > kDrainClocks) return;
 }
 
+// Programmatic launches. grid_wait: until the kernels before this one on the stream have ended and
+// their writes are visible; every CTA calls it before it touches global memory. grid_release: a
+// following launch that waits likewise may be set up from now on.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
