@@ -137,8 +137,9 @@ struct GemmArgs {
     const void* res;  // residual; the backward pass's dh
     int64_t ld_res;
     void* out;
-    void* out2;  // the backward pass's du
-    int64_t ld_out;
+    void* out2;  // the backward pass's du; the second of two products of one A (t_half > 0)
+    int64_t ld_out, ld_out2;
+    int t_half;  // token tiles of the first of two products with the same A; 0: one product
 };
 
 // ------------------------------------------------------------------ activations
@@ -178,12 +179,13 @@ template <> __device__ __forceinline__ float from_f<float>(float v) { return v; 
 // COLS columns (tokens t0 ...) of this warp's 32 lanes. `quad`: which 32 rows of the tile.
 template <int EPI, int ACT, int COLS, typename T, typename O>
 __device__ __forceinline__ void emit(const GemmArgs& g, const float* v, int64_t tile_n, int quad, int lane, int64_t t0,
-                                     float bias) {
+                                     float bias, bool second) {
     const int64_t left = g.M - t0;  // tokens of this block that exist
     if constexpr (EPI == EPI_LINEAR) {
         const int64_t n = tile_n * 128 + quad * 32 + lane;
         const bool in = n < g.N;
-        O* out = (O*)g.out + t0 * g.ld_out + n;
+        const int64_t ld = second ? g.ld_out2 : g.ld_out;
+        O* out = (O*)(second ? g.out2 : g.out) + t0 * ld + n;
         float r[COLS];
         if (g.res) {
             const O* res = (const O*)g.res + t0 * g.ld_res + n;
@@ -195,7 +197,7 @@ __device__ __forceinline__ void emit(const GemmArgs& g, const float* v, int64_t 
         }
 #pragma unroll
         for (int j = 0; j < COLS; ++j)
-            if (in && j < left) out[j * g.ld_out] = from_f<O>(act_fn<ACT>(v[j] + bias) + r[j]);
+            if (in && j < left) out[j * ld] = from_f<O>(act_fn<ACT>(v[j] + bias) + r[j]);
     } else {
         const bool low = lane < 16;
         const int64_t n = tile_n * 64 + quad * 16 + (lane & 15);
@@ -230,12 +232,12 @@ __device__ __forceinline__ void emit(const GemmArgs& g, const float* v, int64_t 
 
 template <int EPI, int COLS, typename T, typename O>
 __device__ __forceinline__ void emit_act(const GemmArgs& g, const float* v, int64_t tile_n, int quad, int lane,
-                                         int64_t t0, float bias) {
+                                         int64_t t0, float bias, bool second) {
     switch (g.act) {
-        case KD_ACT_RELU: emit<EPI, KD_ACT_RELU, COLS, T, O>(g, v, tile_n, quad, lane, t0, bias); break;
-        case KD_ACT_SILU: emit<EPI, KD_ACT_SILU, COLS, T, O>(g, v, tile_n, quad, lane, t0, bias); break;
-        case KD_ACT_GELU: emit<EPI, KD_ACT_GELU, COLS, T, O>(g, v, tile_n, quad, lane, t0, bias); break;
-        default: emit<EPI, KD_ACT_NONE, COLS, T, O>(g, v, tile_n, quad, lane, t0, bias); break;
+        case KD_ACT_RELU: emit<EPI, KD_ACT_RELU, COLS, T, O>(g, v, tile_n, quad, lane, t0, bias, second); break;
+        case KD_ACT_SILU: emit<EPI, KD_ACT_SILU, COLS, T, O>(g, v, tile_n, quad, lane, t0, bias, second); break;
+        case KD_ACT_GELU: emit<EPI, KD_ACT_GELU, COLS, T, O>(g, v, tile_n, quad, lane, t0, bias, second); break;
+        default: emit<EPI, KD_ACT_NONE, COLS, T, O>(g, v, tile_n, quad, lane, t0, bias, second); break;
     }
 }
 
@@ -290,11 +292,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 
     // Tile order: kGroup token tiles together, weight tiles advancing: the CTAs at work at one
     // time then share a few token tiles and a few weight tiles, which L2 serves.
-    auto place = [&](int tile, int& tn, int& tt) {
+    auto place = [&](int tile, int& tn, int& tt) {  // true: a tile of the second product
         const int per = kGroup * g.n_tiles, grp = tile / per, in = tile % per;
         const int size = min(kGroup, g.t_tiles - grp * kGroup);
         tn = in / size;
         tt = grp * kGroup + in % size;
+        const bool second = kBMn && g.t_half > 0 && tt >= g.t_half;
+        if (second) tt -= g.t_half;
+        return second;
     };
 
     if (warp >= 8) {
@@ -311,13 +316,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             bool ok = true, ready = true;  // the ring starts empty
             for (int tile = first; tile < tiles && ok; tile += step) {
                 int tn, tt;
-                place(tile, tn, tt);
+                const bool second = place(tile, tn, tt);
                 const int an = tn * (EPI == EPI_LINEAR ? 128 : 64), bt = tt * bn;
                 int kb = k_lo;
 #pragma unroll
                 for (int seg = 0; seg < 2; ++seg) {  // the first operand pair, the second
                     const int end = seg ? k_hi : min(g.kb0, k_hi);
-                    const CUtensorMap *ma = seg ? &a1 : &a0, *mb = seg ? &b1 : &b0;
+                    const CUtensorMap *ma = seg ? &a1 : &a0, *mb = seg || second ? &b1 : &b0;
                     int k = (kb - (seg ? g.kb0 : 0)) * kBK;
 #pragma unroll 1
                     for (; kb < end && ok; ++kb, k += kBK) {
@@ -407,7 +412,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         bool ok = true;
         for (int tile = first; tile < tiles && ok; tile += step) {
             int tn, tt;
-            place(tile, tn, tt);
+            const bool second = place(tile, tn, tt);
             float bias = 0.f;
             if constexpr (EPI == EPI_LINEAR) {
                 const int64_t n = (int64_t)tn * 128 + quad * 32 + lane;
@@ -424,9 +429,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     for (int j = 0; j < 32; ++j)
                         if (j < n) part[(c + j) * 128 + quad * 32 + lane] = v[j];
                 } else if (g.bn >= 32) {
-                    emit_act<EPI, 32, T, O>(g, v, tn, quad, lane, t0 + c, bias);
+                    emit_act<EPI, 32, T, O>(g, v, tn, quad, lane, t0 + c, bias, second);
                 } else {
-                    emit_act<EPI, 16, T, O>(g, v, tn, quad, lane, t0 + c, bias);
+                    emit_act<EPI, 16, T, O>(g, v, tn, quad, lane, t0 + c, bias, second);
                 }
             };
             auto fetch = [&](uint32_t src, uint32_t* r) {
@@ -484,7 +489,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             cluster_sync_all();
             if (!*dead) {
                 int tn, tt;
-                place(first, tn, tt);
+                const bool second = place(first, tn, tt);
                 const int64_t t0 = (int64_t)tt * g.bn;
                 const int valid = (int)min((int64_t)g.bn, g.M - t0);
                 const int pairs = (valid + 1) / 2;
@@ -509,7 +514,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                             const int64_t n = (int64_t)tn * 128 + quad * 32 + lane;
                             if (g.bias && n < g.N) bias = to_f<T>(((const T*)g.bias)[n]);
                         }
-                        emit_act<EPI, 2, T, O>(g, v, tn, quad, lane, t0 + c, bias);
+                        emit_act<EPI, 2, T, O>(g, v, tn, quad, lane, t0 + c, bias, second);
                     }
                 };
                 if (g.splits == 2) join(std::integral_constant<int, 2>{});
@@ -607,6 +612,8 @@ int operand_map(CUtensorMap* m, int dtype, const Operand& o, int64_t rows, int64
 
 template <int EPI, typename T, typename O>
 int run_typed(GemmArgs g, int dtype, const Operand* a, const Operand* b, int pairs, int64_t k, cudaStream_t stream) {
+    const bool both = pairs < 0;  // two products of a[0], with b[0] into out and b[1] into out2
+    if (both) pairs = 1;
     int sms = 0;
     int rc = op_sm_count(&sms);
     if (rc) return rc;
@@ -614,10 +621,11 @@ int run_typed(GemmArgs g, int dtype, const Operand* a, const Operand* b, int pai
     const int per = gated ? 64 : 128;
     const int64_t n_tiles = (g.N + per - 1) / per;
     const int64_t kblocks = (k + kBK - 1) / kBK;
-    const Plan p = make_plan(n_tiles, g.M, (int)kblocks * (gated ? 1 : pairs), sms, b[0].mn ? 64 : 16);
+    const Plan p = make_plan(both ? 2 * n_tiles : n_tiles, g.M, (int)kblocks * (gated ? 1 : pairs), sms, b[0].mn ? 64 : 16);
     g.kb0 = (int)kblocks;
     g.kb = (int)kblocks * (gated ? 1 : pairs);
-    const int64_t t_tiles = (g.M + p.bn - 1) / p.bn;
+    int64_t t_tiles = (g.M + p.bn - 1) / p.bn;
+    if (both) g.t_half = (int)t_tiles, t_tiles *= 2;
     if (n_tiles * t_tiles > 0x3fffffff) return op_fail(KD_EINVAL, "too many output tiles");
     g.n_tiles = (int)n_tiles;
     g.t_tiles = (int)t_tiles;
@@ -632,6 +640,7 @@ int run_typed(GemmArgs g, int dtype, const Operand* a, const Operand* b, int pai
     if ((rc = operand_map(&mb[0], dtype, b[0], g.M, k, p.bn))) return rc;
     ma[1] = ma[0];
     mb[1] = mb[0];
+    if (both && (rc = operand_map(&mb[1], dtype, b[1], g.M, k, p.bn))) return rc;
     if (pairs > 1) {
         if ((rc = operand_map(&ma[1], dtype, a[1], g.N, k, a_box))) return rc;
         if (!gated && (rc = operand_map(&mb[1], dtype, b[1], g.M, k, p.bn))) return rc;
@@ -803,13 +812,14 @@ int kd_gated_ffn_backward(const kd_gated_args* p, const void* dh, int64_t ld_dh,
         const Operand a[2] = {{q.wg, q.ld_wg, true}, {q.wu, q.ld_wu, true}}, b[2] = {{dg, ld, false}, {du, ld, false}};
         if ((rc = run<EPI_LINEAR>(g, q.dtype, q.dtype, a, b, 2, q.f, s))) return rc;
     }
-    for (int i = 0; i < 2; ++i) {  // dwg[f][c] = sum_t dg[t][f] x[t][c]
-        void* dw = i ? dwu : dwg;
-        if (!dw) continue;
+    // dwg[f][c] = sum_t dg[t][f] x[t][c], dwu from du: one launch for both
+    const Operand a{q.x, q.ld_x, true}, b[2] = {{dwg ? dg : du, ld, true}, {du, ld, true}};
+    if (dwg || dwu) {
         GemmArgs g{};
-        g.N = q.d, g.M = q.f, g.out = dw, g.ld_out = i ? ld_dwu : ld_dwg;
-        const Operand a{q.x, q.ld_x, true}, b{i ? du : dg, ld, true};
-        if ((rc = run<EPI_LINEAR>(g, q.dtype, q.dtype, &a, &b, 1, q.m, s))) return rc;
+        g.N = q.d, g.M = q.f;
+        g.out = dwg ? dwg : dwu, g.ld_out = dwg ? ld_dwg : ld_dwu;
+        g.out2 = dwu, g.ld_out2 = ld_dwu;
+        if ((rc = run<EPI_LINEAR>(g, q.dtype, q.dtype, &a, b, dwg && dwu ? -1 : 1, q.m, s))) return rc;
     }
     return KD_OK;
 }
