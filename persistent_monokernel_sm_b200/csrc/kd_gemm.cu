@@ -76,13 +76,16 @@ static EncodeFn encode_fn() {
 }
 
 static int encode(CUtensorMap* m, int dtype, const void* base, int rank, const cuuint64_t* dims,
-                  const cuuint64_t* strides, const cuuint32_t* box) {
+                  const cuuint64_t* strides, const cuuint32_t* box, bool swizzle = true) {
     EncodeFn f = encode_fn();
     if (!f) return op_fail(KD_ECUDA, "the driver has no cuTensorMapEncodeTiled");
     const cuuint32_t ones[3] = {1, 1, 1};
-    const CUresult r = f(m, dtype == KD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                         (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, ones,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    const CUtensorMapDataType type = dtype == KD_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : dtype == KD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const CUresult r = f(m, type, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, ones,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return op_fail(KD_ECUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
     return KD_OK;
@@ -94,6 +97,15 @@ int make_map_2d(CUtensorMap* m, int dtype, const void* base, int64_t cols, int64
     const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
     const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
     return encode(m, dtype, base, 2, dims, strides, box);
+}
+
+// Of an output: boxes as they lie in shared memory, without a swizzle.
+static int make_map_out(CUtensorMap* m, int dtype, const void* base, int64_t cols, int64_t rows, int64_t ld,
+                        int box_cols, int box_rows) {
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * (dtype == KD_F32 ? 4 : 2)};
+    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+    return encode(m, dtype, base, 2, dims, strides, box, false);
 }
 
 int make_map_3d(CUtensorMap* m, int dtype, const void* base, int64_t c0, int64_t c1, int64_t c2, int64_t ld1,
@@ -118,7 +130,13 @@ constexpr int kChunk = 8;  // 64-deep k-blocks
 constexpr int kBK = 64;            // k-block: 128 bytes of a row
 constexpr int kABytes = 128 * kBK * 2;
 constexpr int kMaxRing = 12;
-constexpr int kRingBytes = 216 * 1024;
+constexpr int kRingBytes = 192 * 1024;
+// Behind the ring: 4 KB for each epilogue warp, two halves in turn, from which TMA writes the
+// output. A column of the accumulator is then one store to shared memory, with no address to
+// compute; stored to global memory from the lanes it took 28 instructions, and a 128 x 256 tile
+// 9 us where its products take 13 (at k = 2,048).
+constexpr int kStageBytes = 4096;
+constexpr int kSmemBytes = 1024 + kRingBytes + 8 * kStageBytes;
 constexpr int kGroup = 8;  // token tiles that are taken together while the weight tiles advance
 
 // Which index of the two operands is the contiguous one in memory: k of both; the feature of A
@@ -139,6 +157,7 @@ struct GemmArgs {
     void* out;
     void* out2;  // the backward pass's du; the second of two products of one A (t_half > 0)
     int64_t ld_out, ld_out2;
+    int tma_out;  // outputs by TMA (aligned rows), else from the lanes
     int t_half;  // token tiles of the first of two products with the same A; 0: one product
 };
 
@@ -176,68 +195,142 @@ template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }
 template <typename T> __device__ __forceinline__ T from_f(float v) { return Half2<T>::down(v); }
 template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
 
-// COLS columns (tokens t0 ...) of this warp's 32 lanes. `quad`: which 32 rows of the tile.
+// A warp's way out of the accumulators.
+struct Out {
+    const CUtensorMap *o0, *o1;
+    uint8_t* stage;  // this warp's 4 KB of shared memory
+    int flip;        // the half that is used next
+    int quad, lane;
+};
+
+// Rows (tokens) of a box: two boxes of 16 fp32 columns, one of 32 of 16 bits.
+template <int COLS, typename O> struct Box { static constexpr int rows = sizeof(O) == 4 || COLS < 32 ? 16 : 32; };
+
+// Only boxes whose columns all exist go this way: TMA writes whole 16 bytes, also past the end of
+// a row that is no multiple of them (rows of a box past the last token are left out exactly).
+
+// The half of the stage that the store before the last has left; then, once the warp has filled
+// it, its way to global memory.
+__device__ __forceinline__ uint8_t* stage_open(Out& w) {
+    if (w.lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    __syncwarp();
+    uint8_t* p = w.stage + w.flip * (kStageBytes / 2);
+    w.flip ^= 1;
+    return p;
+}
+__device__ __forceinline__ void stage_store(const Out& w, const CUtensorMap* m, const uint8_t* from, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(m), "r"(x), "r"(y),
+                 "r"(smem_u32(from))
+                 : "memory");
+}
+__device__ __forceinline__ void stage_fence() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+}
+__device__ __forceinline__ void stage_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+
+// COLS columns (tokens t0 ...) of this warp's 32 lanes; w.quad: which 32 rows of the tile.
 template <int EPI, int ACT, int COLS, typename T, typename O>
-__device__ __forceinline__ void emit(const GemmArgs& g, const float* v, int64_t tile_n, int quad, int lane, int64_t t0,
-                                     float bias, bool second) {
-    const int64_t left = g.M - t0;  // tokens of this block that exist
+__device__ __forceinline__ void emit(const GemmArgs& g, Out& w, const float* v, int tile_n, int64_t t0, float bias,
+                                     bool second) {
+    const int lane = w.lane;
     if constexpr (EPI == EPI_LINEAR) {
-        const int64_t n = tile_n * 128 + quad * 32 + lane;
-        const bool in = n < g.N;
-        const int64_t ld = second ? g.ld_out2 : g.ld_out;
-        O* out = (O*)(second ? g.out2 : g.out) + t0 * ld + n;
+        const int n0 = tile_n * 128 + w.quad * 32, n = n0 + lane;
+        if (n0 >= g.N) return;
+        const int left = n < g.N ? (int)min((int64_t)COLS, g.M - t0) : 0;  // columns that exist
         float r[COLS];
         if (g.res) {
             const O* res = (const O*)g.res + t0 * g.ld_res + n;
 #pragma unroll
-            for (int j = 0; j < COLS; ++j) r[j] = in && j < left ? to_f<O>(res[j * g.ld_res]) : 0.f;
+            for (int j = 0; j < COLS; ++j, res += g.ld_res) r[j] = j < left ? to_f<O>(*res) : 0.f;
+#pragma unroll
+            for (int j = 0; j < COLS; ++j) r[j] = act_fn<ACT>(v[j] + bias) + r[j];
         } else {
 #pragma unroll
-            for (int j = 0; j < COLS; ++j) r[j] = 0.f;
+            for (int j = 0; j < COLS; ++j) r[j] = act_fn<ACT>(v[j] + bias);
         }
+        if (COLS >= 16 && g.tma_out && n0 + 32 <= g.N) {
+            constexpr int R = Box<COLS, O>::rows;
 #pragma unroll
-        for (int j = 0; j < COLS; ++j)
-            if (in && j < left) out[j * ld] = from_f<O>(act_fn<ACT>(v[j] + bias) + r[j]);
+            for (int c = 0; c < COLS; c += R) {
+                uint8_t* p = stage_open(w);
+                O* q = reinterpret_cast<O*>(p) + lane;
+#pragma unroll
+                for (int j = 0; j < R; ++j) q[j * 32] = from_f<O>(r[c + j]);
+                stage_fence();
+                if (lane == 0 && t0 + c < g.M) stage_store(w, second ? w.o1 : w.o0, p, n0, (int)t0 + c);
+                if (lane == 0) stage_commit();
+            }
+        } else {
+            const int64_t ld = second ? g.ld_out2 : g.ld_out;
+            O* out = (O*)(second ? g.out2 : g.out) + t0 * ld + n;
+#pragma unroll
+            for (int j = 0; j < COLS; ++j, out += ld)
+                if (j < left) *out = from_f<O>(r[j]);
+        }
     } else {
+        // Lanes 0-15 hold gate rows, 16-31 the up rows of the same features: of columns 2j and
+        // 2j + 1 the lower lanes finish the first, the upper ones the second.
         const bool low = lane < 16;
-        const int64_t n = tile_n * 64 + quad * 16 + (lane & 15);
-        const bool in = n < g.N;
+        const int n0 = tile_n * 64 + w.quad * 16, n = n0 + (lane & 15);
+        if (n0 >= g.N) return;
         const int64_t at = t0 + (low ? 0 : 1);
+        const int left = n < g.N ? (int)min((int64_t)COLS, g.M - at) : 0;
         T dh[COLS / 2];
         if constexpr (EPI == EPI_GATED_BWD) {
             const T* p = (const T*)g.res + at * g.ld_res + n;
 #pragma unroll
-            for (int j = 0; j < COLS / 2; ++j)
-                dh[j] = in && at + 2 * j < g.M ? p[2 * j * g.ld_res] : from_f<T>(0.f);
+            for (int j = 0; j < COLS; j += 2, p += 2 * g.ld_res) dh[j / 2] = j < left ? *p : from_f<T>(0.f);
         }
+        const bool staged = COLS >= 16 && g.tma_out && n0 + 16 <= g.N;
+        uint8_t* p = staged ? stage_open(w) : nullptr;
+        T *q0 = reinterpret_cast<T*>(p) + lane, *q1 = q0 + 512;  // [token][16 features]: 32 lanes, two rows
+        const int64_t ld = g.ld_out;
+        T *out = (T*)g.out + at * ld + n, *out2 = (T*)g.out2 + at * ld + n;
 #pragma unroll
-        for (int j = 0; j < COLS / 2; ++j) {
-            const float a = v[2 * j], b = v[2 * j + 1];
-            const float got = __shfl_xor_sync(0xffffffffu, low ? b : a, 16);
-            const float gate = low ? a : got, up = low ? got : b;
-            if (!in || at + 2 * j >= g.M) continue;
-            const int64_t o = (at + 2 * j) * g.ld_out + n;
+        for (int j = 0; j < COLS; j += 2) {
+            const float got = __shfl_xor_sync(0xffffffffu, low ? v[j + 1] : v[j], 16);
+            const float gate = low ? v[j] : got, up = low ? got : v[j + 1];
+            float a, b = 0.f;
             if constexpr (EPI == EPI_GATED) {
-                ((T*)g.out)[o] = from_f<T>(act_fn<ACT>(gate) * up);
+                a = act_fn<ACT>(gate) * up;
             } else {
                 float f, s;
                 act_slope<ACT>(gate, &f, &s);
-                const float d = to_f<T>(dh[j]);
-                ((T*)g.out)[o] = from_f<T>(d * up * s);
-                ((T*)g.out2)[o] = from_f<T>(d * f);
+                const float d = to_f<T>(dh[j / 2]);
+                a = d * up * s, b = d * f;
             }
+            if (staged) {
+                q0[j * 16] = from_f<T>(a);
+                if constexpr (EPI == EPI_GATED_BWD) q1[j * 16] = from_f<T>(b);
+            } else {
+                if (j < left) {
+                    *out = from_f<T>(a);
+                    if constexpr (EPI == EPI_GATED_BWD) *out2 = from_f<T>(b);
+                }
+                out += 2 * ld;
+                if constexpr (EPI == EPI_GATED_BWD) out2 += 2 * ld;
+            }
+        }
+        if (staged) {
+            stage_fence();
+            if (lane == 0 && t0 < g.M) {
+                stage_store(w, w.o0, p, n0, (int)t0);
+                if constexpr (EPI == EPI_GATED_BWD) stage_store(w, w.o1, p + 1024, n0, (int)t0);
+            }
+            if (lane == 0) stage_commit();
         }
     }
 }
 
 template <int EPI, int COLS, typename T, typename O>
-__device__ __forceinline__ void emit_act(const GemmArgs& g, const float* v, int64_t tile_n, int quad, int lane,
-                                         int64_t t0, float bias, bool second) {
+__device__ __forceinline__ void emit_act(const GemmArgs& g, Out& w, const float* v, int tile_n, int64_t t0, float bias,
+                                         bool second) {
     switch (g.act) {
-        case KD_ACT_RELU: emit<EPI, KD_ACT_RELU, COLS, T, O>(g, v, tile_n, quad, lane, t0, bias, second); break;
-        case KD_ACT_SILU: emit<EPI, KD_ACT_SILU, COLS, T, O>(g, v, tile_n, quad, lane, t0, bias, second); break;
-        case KD_ACT_GELU: emit<EPI, KD_ACT_GELU, COLS, T, O>(g, v, tile_n, quad, lane, t0, bias, second); break;
-        default: emit<EPI, KD_ACT_NONE, COLS, T, O>(g, v, tile_n, quad, lane, t0, bias, second); break;
+        case KD_ACT_RELU: emit<EPI, KD_ACT_RELU, COLS, T, O>(g, w, v, tile_n, t0, bias, second); break;
+        case KD_ACT_SILU: emit<EPI, KD_ACT_SILU, COLS, T, O>(g, w, v, tile_n, t0, bias, second); break;
+        case KD_ACT_GELU: emit<EPI, KD_ACT_GELU, COLS, T, O>(g, w, v, tile_n, t0, bias, second); break;
+        default: emit<EPI, KD_ACT_NONE, COLS, T, O>(g, w, v, tile_n, t0, bias, second); break;
     }
 }
 
@@ -246,6 +339,7 @@ template <int EPI, int LAY, typename T, typename O>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUtensorMap a1,
                 const __grid_constant__ CUtensorMap b0, const __grid_constant__ CUtensorMap b1,
+                const __grid_constant__ CUtensorMap o0, const __grid_constant__ CUtensorMap o1,
                 const __grid_constant__ GemmArgs g) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t s_full[kMaxRing], s_empty[kMaxRing], s_tfull[2], s_tempty[2], s_drain;
@@ -408,6 +502,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         set_regs_up<kEpiRegs>();
         const int quad = warp & 3, half = warp >> 2;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        Out w{&o0, &o1, smem_raw + (ring - smem_u32(smem_raw)) + kRingBytes + warp * kStageBytes, 0, quad, lane};
         int local = 0;
         bool ok = true;
         for (int tile = first; tile < tiles && ok; tile += step) {
@@ -429,9 +524,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     for (int j = 0; j < 32; ++j)
                         if (j < n) part[(c + j) * 128 + quad * 32 + lane] = v[j];
                 } else if (g.bn >= 32) {
-                    emit_act<EPI, 32, T, O>(g, v, tn, quad, lane, t0 + c, bias, second);
+                    emit_act<EPI, 32, T, O>(g, w, v, tn, t0 + c, bias, second);
                 } else {
-                    emit_act<EPI, 16, T, O>(g, v, tn, quad, lane, t0 + c, bias, second);
+                    emit_act<EPI, 16, T, O>(g, w, v, tn, t0 + c, bias, second);
                 }
             };
             auto fetch = [&](uint32_t src, uint32_t* r) {
@@ -514,7 +609,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                             const int64_t n = (int64_t)tn * 128 + quad * 32 + lane;
                             if (g.bias && n < g.N) bias = to_f<T>(((const T*)g.bias)[n]);
                         }
-                        emit_act<EPI, 2, T, O>(g, v, tn, quad, lane, t0 + c, bias, second);
+                        w.quad = quad;
+                        emit_act<EPI, 2, T, O>(g, w, v, tn, t0 + c, bias, second);
                     }
                 };
                 if (g.splits == 2) join(std::integral_constant<int, 2>{});
@@ -524,6 +620,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             __syncwarp();
             cluster_sync_all();
         }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // its outputs are out
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
@@ -575,22 +673,20 @@ Plan make_plan(int64_t n_tiles, int64_t M, int kb, int sms, int min_bn) {
 }
 
 template <int EPI, int LAY, typename T, typename O>
-int launch(const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0, const CUtensorMap& b1, const GemmArgs& g,
-           int grid, cudaStream_t stream) {
-    const int smem = g.stages * (kABytes + g.bn * kBK * 2) + 1024;
+int launch(const CUtensorMap* m, const GemmArgs& g, int grid, cudaStream_t stream) {
     int dev = 0;
     cudaGetDevice(&dev);
     static std::atomic<bool> ready[64];
     if (dev >= 64 || !ready[dev].load()) {
         cudaError_t e = cudaFuncSetAttribute(gemm_kernel<EPI, LAY, T, O>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             kRingBytes + 1024);
+                                             kSmemBytes);
         if (e != cudaSuccess) return op_fail(KD_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
         if (dev < 64) ready[dev].store(true);
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kGemmThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = stream;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -600,7 +696,7 @@ int launch(const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0, 
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = g.splits > 1 ? 2 : 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_kernel<EPI, LAY, T, O>, a0, a1, b0, b1, g);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_kernel<EPI, LAY, T, O>, m[0], m[1], m[2], m[3], m[4], m[5], g);
     if (e != cudaSuccess) return op_fail(KD_ECUDA, "launch failed: %s", cudaGetErrorString(e));
     return KD_OK;
 }
@@ -634,22 +730,36 @@ int run_typed(GemmArgs g, int dtype, const Operand* a, const Operand* b, int pai
     g.stages = kRingBytes / (kABytes + p.bn * kBK * 2);
     if (g.stages > kMaxRing) g.stages = kMaxRing;
     g.idesc = make_idesc(128, p.bn, dtype == KD_BF16, a[0].mn, b[0].mn);
-    CUtensorMap ma[2], mb[2];
+    CUtensorMap m[6];  // A, A of the second pair, B, the second B, the outputs
     const int a_box = gated ? 16 : 128;
-    if ((rc = operand_map(&ma[0], dtype, a[0], g.N, k, a_box))) return rc;
-    if ((rc = operand_map(&mb[0], dtype, b[0], g.M, k, p.bn))) return rc;
-    ma[1] = ma[0];
-    mb[1] = mb[0];
-    if (both && (rc = operand_map(&mb[1], dtype, b[1], g.M, k, p.bn))) return rc;
-    if (pairs > 1) {
-        if ((rc = operand_map(&ma[1], dtype, a[1], g.N, k, a_box))) return rc;
-        if (!gated && (rc = operand_map(&mb[1], dtype, b[1], g.M, k, p.bn))) return rc;
+    if ((rc = operand_map(&m[0], dtype, a[0], g.N, k, a_box))) return rc;
+    if ((rc = operand_map(&m[2], dtype, b[0], g.M, k, p.bn))) return rc;
+    m[1] = m[0];
+    m[3] = m[2];
+    if (pairs > 1 && (rc = operand_map(&m[1], dtype, a[1], g.N, k, a_box))) return rc;
+    if ((both || (pairs > 1 && !gated)) && (rc = operand_map(&m[3], dtype, b[1], g.M, k, p.bn))) return rc;
+    const bool two = both || EPI == EPI_GATED_BWD;
+    const int out_type = sizeof(O) == 4 ? KD_F32 : dtype;
+    if (!two) g.ld_out2 = g.ld_out, g.out2 = g.out;
+    if (EPI == EPI_GATED_BWD) g.ld_out2 = g.ld_out;
+    int64_t ld[2] = {g.ld_out, g.ld_out2};
+    const void* out[2] = {g.out, g.out2};
+    g.tma_out = 1;
+    for (int i = 0; i < 2; ++i) {
+        if (g.M == 1) ld[i] = (g.N + 7) & ~(int64_t)7;  // one row: its distance to the next is not used
+        if ((uintptr_t)out[i] % 16 || ld[i] * (int64_t)sizeof(O) % 16 || ld[i] >= (int64_t)1 << 37) g.tma_out = 0;
+    }
+    m[4] = m[5] = m[0];
+    if (g.tma_out && p.splits == 1) {
+        const int rows = sizeof(O) == 4 || p.bn < 32 ? 16 : 32;
+        if ((rc = make_map_out(&m[4], out_type, out[0], g.N, g.M, ld[0], gated ? 16 : 32, rows))) return rc;
+        if (two && (rc = make_map_out(&m[5], out_type, out[1], g.N, g.M, ld[1], gated ? 16 : 32, rows))) return rc;
     }
     if constexpr (EPI == EPI_LINEAR) {
-        if (b[0].mn) return launch<EPI, LAY_MM, T, O>(ma[0], ma[1], mb[0], mb[1], g, p.grid, stream);
-        if (a[0].mn) return launch<EPI, LAY_MK, T, O>(ma[0], ma[1], mb[0], mb[1], g, p.grid, stream);
+        if (b[0].mn) return launch<EPI, LAY_MM, T, O>(m, g, p.grid, stream);
+        if (a[0].mn) return launch<EPI, LAY_MK, T, O>(m, g, p.grid, stream);
     }
-    return launch<EPI, LAY_KK, T, O>(ma[0], ma[1], mb[0], mb[1], g, p.grid, stream);
+    return launch<EPI, LAY_KK, T, O>(m, g, p.grid, stream);
 }
 
 template <int EPI>
