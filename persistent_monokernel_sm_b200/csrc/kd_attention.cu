@@ -181,7 +181,8 @@ __global__ void __launch_bounds__(kThr, 1)
     __syncthreads();
     tc_fence_after();
     grid_wait();
-    grid_release();
+    // Not before a join: its CTAs would wait on the few SMs that are free now and run there alone.
+    if (a.splits == 1) grid_release();
     const uint32_t tmem = s_tmem;  // columns: S0, S1 (128 each), O0, O1 (HD each)
 
     if (warp >= 8) {
@@ -561,12 +562,19 @@ Cut cut_of(int64_t n, int64_t kv_len, int r, int hkv, int hd) {
     const int64_t tiles = (n + tq - 1) / tq, units = tiles * hkv, pairs = (tiles + 1) / 2 * hkv;
     const int64_t blocks = (kv_len + n + kKeys - 1) / kKeys;
     Cut c{0, 1, pairs, 0};
-    if (units <= kCtas) {
-        // One tile per CTA, and its blocks over as many CTAs as there are SMs while each keeps
-        // two blocks for either stream (one: the join then costs more than it saves).
+    // Full waves of CTAs, in tiles: rows of about the same length that just miss a whole wave of
+    // pairs are better off as single tiles (1,184 tokens behind 31,000, 32/8 heads: 152 pairs 786
+    // us, 304 single tiles 496 us). Shorter rows among longer ones even the pairs out by themselves.
+    const int64_t pair_waves = (pairs + kCtas - 1) / kCtas, unit_waves = (units + kCtas - 1) / kCtas;
+    if (units <= kCtas || (kv_len >= n && pair_waves <= 4 && unit_waves < 2 * pair_waves)) {
+        // One tile per CTA; few tiles' blocks go to as many CTAs as there are SMs while each of its
+        // streams keeps a block (one token behind 2,000, 16/8 heads: whole 16.6 us, by eight 9.9; one
+        // behind 32,768: by eight 37, by eighteen 31). Past sixteen, a CTA keeps six blocks: the join
+        // reads every share (one token behind 32,768, 8/1 heads: by 36 19 us, by 128 28).
         c.shared = 1;
-        const int64_t most = kCtas / units, worth = blocks / 4;
-        c.splits = (int)(most < worth ? most : worth);
+        int64_t most = blocks / 6 > 16 ? blocks / 6 : 16;
+        if (most > kCtas / units) most = kCtas / units;
+        c.splits = (int)(most < blocks / 2 ? most : blocks / 2);
         if (c.splits < 1) c.splits = 1;
         c.grid = units * c.splits;
         if (c.splits > 1) c.bytes = c.grid * 128 * (hd + 4) * 4 + 256;
