@@ -647,13 +647,15 @@ struct Plan {
     int bn, splits, grid;
 };
 
-Plan make_plan(int64_t n_tiles, int64_t M, int kb, int sms, int min_bn) {
+// room[s]: clusters of s CTAs that the device runs at once (a GPU processing cluster holds whole ones:
+// fewer than sms / s; 128 CTAs in clusters of eight take two rounds).
+Plan make_plan(int64_t n_tiles, int64_t M, int kb, int sms, const int* room, int min_bn) {
     Plan best{};
     double best_cost = 1e300;
     for (int bn = min_bn; bn <= 256; bn *= 2) {
         const int64_t tiles = n_tiles * ((M + bn - 1) / bn);
         for (int s = 1; s <= 8; s *= 2) {
-            if (s > 1 && (2 * s > kb || tiles * s > sms)) break;
+            if (s > 1 && (2 * s > kb || tiles > room[s])) break;
             const double work = bn <= 64 ? 0.20 + bn * 0.0003 : bn == 128 ? 0.28 : 0.41;
             const double ctas = (double)(tiles * s < sms ? tiles * s : sms);
             const double load = ctas * (kABytes + 128.0 * bn) / 10.5e6;
@@ -701,6 +703,36 @@ int launch(const CUtensorMap* m, const GemmArgs& g, int grid, cudaStream_t strea
     return KD_OK;
 }
 
+int cluster_room(int sms, int room[9]) {
+    static std::atomic<int> cached[64][3];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return op_fail(KD_ECUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
+    for (int i = 0, s = 2; s <= 8; ++i, s *= 2) {
+        int n = dev < 64 ? cached[dev][i].load() : 0;
+        if (n == 0) {
+            const auto kernel = gemm_kernel<EPI_LINEAR, LAY_KK, __nv_bfloat16, __nv_bfloat16>;
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3(sms / s * s);
+            cfg.blockDim = dim3(kGemmThreads);
+            cfg.dynamicSmemBytes = kSmemBytes;
+            cudaLaunchAttribute at[1];
+            at[0].id = cudaLaunchAttributeClusterDimension;
+            at[0].val.clusterDim.x = s;
+            at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+            cfg.attrs = at;
+            cfg.numAttrs = 1;
+            if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+            if (e != cudaSuccess) return op_fail(KD_ECUDA, "cudaOccupancyMaxActiveClusters: %s", cudaGetErrorString(e));
+            if (n < 1) n = -1;  // none: not asked again
+            if (dev < 64) cached[dev][i].store(n);
+        }
+        room[s] = n;
+    }
+    return KD_OK;
+}
+
 int operand_map(CUtensorMap* m, int dtype, const Operand& o, int64_t rows, int64_t k, int box_rows) {
     if (o.mn) return make_map_2d(m, dtype, o.p, rows, k, o.ld, 64, kBK);
     return make_map_2d(m, dtype, o.p, k, rows, o.ld, kBK, box_rows);
@@ -711,13 +743,15 @@ int run_typed(GemmArgs g, int dtype, const Operand* a, const Operand* b, int pai
     const bool both = pairs < 0;  // two products of a[0], with b[0] into out and b[1] into out2
     if (both) pairs = 1;
     int sms = 0;
+    int room[9];
     int rc = op_sm_count(&sms);
+    if (rc == KD_OK) rc = cluster_room(sms, room);
     if (rc) return rc;
     const bool gated = EPI != EPI_LINEAR;
     const int per = gated ? 64 : 128;
     const int64_t n_tiles = (g.N + per - 1) / per;
     const int64_t kblocks = (k + kBK - 1) / kBK;
-    const Plan p = make_plan(both ? 2 * n_tiles : n_tiles, g.M, (int)kblocks * (gated ? 1 : pairs), sms, b[0].mn ? 64 : 16);
+    const Plan p = make_plan(both ? 2 * n_tiles : n_tiles, g.M, (int)kblocks * (gated ? 1 : pairs), sms, room, b[0].mn ? 64 : 16);
     g.kb0 = (int)kblocks;
     g.kb = (int)kblocks * (gated ? 1 : pairs);
     int64_t t_tiles = (g.M + p.bn - 1) / p.bn;
