@@ -1,13 +1,17 @@
-"""Build libkd.so in-tree for sm_100a with nvcc (no JIT cache, no torch extension)."""
+"""Build libkd.so in-tree for sm_100a with nvcc, and _kd_torch.so, the operators on torch tensors, with
+g++ against it (no JIT cache)."""
 
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libkd.so")
+TORCH_OUT = os.path.join(HERE, "_kd_torch.so")
+TORCH_SOURCE = os.path.join(CSRC, "kd_torch.cpp")
 SOURCES = ["kd_kernel.cu", "kd_api.cu", "kd_noalloc.cu", "kd_gemm.cu", "kd_attention.cu",
            "kd_prefill.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
@@ -22,24 +26,51 @@ def _stale(out, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", "kd.h"),
-                                                                  os.path.abspath(__file__)]
+def _build_lib(force, verbose):
+    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if not f.endswith(".cpp")]
+    deps += [os.path.join(ROOT, "include", "kd.h"), os.path.abspath(__file__)]
     if not force and not _stale(OUT, deps):
-        return OUT
+        return
     bdir = os.path.join(ROOT, "_build")
     os.makedirs(bdir, exist_ok=True)
-    objs = []
+    jobs = []
     for src in SOURCES:
         obj = os.path.join(bdir, src.replace(".cu", ".o"))
         cmd = [NVCC, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
-        subprocess.check_call(cmd)
-        objs.append(obj)
+        jobs.append((obj, cmd, subprocess.Popen(cmd)))
+    failed = [cmd for _, cmd, p in jobs if p.wait() != 0]
+    if failed:
+        raise subprocess.CalledProcessError(1, failed[0])
     tmp = OUT + ".tmp%d" % os.getpid()
-    subprocess.check_call([NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", tmp, *objs])
+    subprocess.check_call([NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", tmp,
+                           *[obj for obj, _, _ in jobs]])
     os.replace(tmp, OUT)
+
+
+def _build_torch(force):
+    deps = [TORCH_SOURCE, os.path.join(ROOT, "include", "kd.h"), os.path.abspath(__file__)]
+    if not force and not _stale(TORCH_OUT, deps):
+        return
+    import torch
+    from torch.utils import cpp_extension
+    include = ["-isystem" + p for p in cpp_extension.include_paths() + [sysconfig.get_paths()["include"],
+                                                                        os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")]]
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = TORCH_OUT + ".tmp%d" % os.getpid()
+    # libkd.so is found beside the module, torch's libraries where torch has loaded them
+    subprocess.check_call([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+                           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+                           "-I" + os.path.join(ROOT, "include"), *include, TORCH_SOURCE, "-o", tmp, "-L" + HERE, "-l:libkd.so",
+                           "-L" + lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+                           "-Wl,-rpath,$ORIGIN"])
+    os.replace(tmp, TORCH_OUT)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    _build_lib(force, verbose)
+    _build_torch(force)
     return OUT
 
 

@@ -1,8 +1,6 @@
 """The prompt operators' refusals and workspace sizes, without a GPU: arguments are checked on the
 host before a device is touched."""
 
-import ctypes
-
 import pytest
 import torch
 
@@ -112,15 +110,6 @@ def test_workspaces():
     assert kd.load_library().kd_prefill(None, None, 1, 0, None, 0) == -1
 
 
-def test_packed_structs_are_the_header_s():
-    from persistent_monokernel_sm_b200 import operators as o
-    for packed, struct in ((o._LINEAR, kd.kd_linear_args), (o._GATED, kd.kd_gated_args), (o._ATTENTION, kd.kd_attention_args)):
-        n = len(struct._fields_)
-        values = [float(i + 1) if t is ctypes.c_float else i + 1 for i, (_, t) in enumerate(struct._fields_)]
-        s = struct.from_buffer_copy(packed.pack(*values).ljust(ctypes.sizeof(struct), b"\0"))
-        assert [getattr(s, f) for f, _ in struct._fields_] == values and len(values) == n
-
-
 def test_tensors_are_checked():
     x, w = torch.zeros(2, 8, dtype=torch.bfloat16), torch.zeros(4, 8, dtype=torch.bfloat16)
     for call in (lambda: kd.linear(x, w), lambda: kd.linear(None, w), lambda: kd.linear([1], w), lambda: kd.gated_ffn(x, w, w),
@@ -128,3 +117,6 @@ def test_tensors_are_checked():
         with pytest.raises(kd.KdError) as e:
             call()
         assert e.value.code == -1
+        assert len(str(e.value)) > 20
+    with pytest.raises(TypeError):
+        kd.linear(x)
