@@ -232,14 +232,17 @@ __device__ __forceinline__ void stage_commit() { asm volatile("cp.async.bulk.com
 // COLS columns (tokens t0 ...) of this warp's 32 lanes; w.quad: which 32 rows of the tile.
 template <int EPI, int ACT, int COLS, typename T, typename O>
 __device__ __forceinline__ void emit(const GemmArgs& g, Out& w, const float* v, int tile_n, int64_t t0, float bias,
-                                     bool second) {
+                                     bool second, const float* given) {
     const int lane = w.lane;
     if constexpr (EPI == EPI_LINEAR) {
         const int n0 = tile_n * 128 + w.quad * 32, n = n0 + lane;
         if (n0 >= g.N) return;
         const int left = n < g.N ? (int)min((int64_t)COLS, g.M - t0) : 0;  // columns that exist
         float r[COLS];
-        if (g.res) {
+        if (COLS == 2) {
+#pragma unroll
+            for (int j = 0; j < COLS; ++j) r[j] = act_fn<ACT>(v[j] + bias) + given[j];
+        } else if (g.res) {
             const O* res = (const O*)g.res + t0 * g.ld_res + n;
 #pragma unroll
             for (int j = 0; j < COLS; ++j, res += g.ld_res) r[j] = j < left ? to_f<O>(*res) : 0.f;
@@ -323,14 +326,14 @@ __device__ __forceinline__ void emit(const GemmArgs& g, Out& w, const float* v, 
     }
 }
 
-template <int EPI, int COLS, typename T, typename O>
+template <int EPI, int LAY, int COLS, typename T, typename O>
 __device__ __forceinline__ void emit_act(const GemmArgs& g, Out& w, const float* v, int tile_n, int64_t t0, float bias,
-                                         bool second) {
-    switch (g.act) {
-        case KD_ACT_RELU: emit<EPI, KD_ACT_RELU, COLS, T, O>(g, w, v, tile_n, t0, bias, second); break;
-        case KD_ACT_SILU: emit<EPI, KD_ACT_SILU, COLS, T, O>(g, w, v, tile_n, t0, bias, second); break;
-        case KD_ACT_GELU: emit<EPI, KD_ACT_GELU, COLS, T, O>(g, w, v, tile_n, t0, bias, second); break;
-        default: emit<EPI, KD_ACT_NONE, COLS, T, O>(g, w, v, tile_n, t0, bias, second); break;
+                                         bool second, const float* given = nullptr) {
+    switch (LAY == LAY_MM ? KD_ACT_NONE : g.act) {
+        case KD_ACT_RELU: emit<EPI, KD_ACT_RELU, COLS, T, O>(g, w, v, tile_n, t0, bias, second, given); break;
+        case KD_ACT_SILU: emit<EPI, KD_ACT_SILU, COLS, T, O>(g, w, v, tile_n, t0, bias, second, given); break;
+        case KD_ACT_GELU: emit<EPI, KD_ACT_GELU, COLS, T, O>(g, w, v, tile_n, t0, bias, second, given); break;
+        default: emit<EPI, KD_ACT_NONE, COLS, T, O>(g, w, v, tile_n, t0, bias, second, given); break;
     }
 }
 
@@ -524,9 +527,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     for (int j = 0; j < 32; ++j)
                         if (j < n) part[(c + j) * 128 + quad * 32 + lane] = v[j];
                 } else if (g.bn >= 32) {
-                    emit_act<EPI, 32, T, O>(g, w, v, tn, t0 + c, bias, second);
+                    emit_act<EPI, LAY, 32, T, O>(g, w, v, tn, t0 + c, bias, second);
                 } else {
-                    emit_act<EPI, 16, T, O>(g, w, v, tn, t0 + c, bias, second);
+                    emit_act<EPI, LAY, 16, T, O>(g, w, v, tn, t0 + c, bias, second);
                 }
             };
             auto fetch = [&](uint32_t src, uint32_t* r) {
@@ -591,26 +594,40 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 // Every CTA's share of a pair of columns is asked for before the first is used.
                 auto join = [&](auto count) {
                     constexpr int S = decltype(count)::value;
-                    for (int u = rank * 8 + warp; u < 4 * pairs; u += 8 * S) {
-                        const int quad = u & 3, c = (u >> 2) * 2;
-                        const uint32_t at = ring + (uint32_t)(c * 128 + quad * 32 + lane) * 4;
-                        float part[S][2];
+                    // two pairs at a time, with what the epilogue adds to them
+                    for (int u0 = rank * 8 + warp; u0 < 4 * pairs; u0 += 16 * S) {
+                        float part[2][S][2], add[2][2], bias[2];
 #pragma unroll
-                        for (int s = 0; s < S; ++s) {
-                            const uint32_t ra = map_rank(at, s);
-                            part[s][0] = ld_cluster_f32(ra);
-                            part[s][1] = ld_cluster_f32(ra + 512);
-                        }
-                        float v[2] = {part[0][0], part[0][1]};
+                        for (int i = 0; i < 2; ++i) {
+                            const int u = min(u0 + i * 8 * S, 4 * pairs - 1), quad = u & 3, c = (u >> 2) * 2;
+                            bias[i] = add[i][0] = add[i][1] = 0.f;
+                            if constexpr (EPI == EPI_LINEAR) {
+                                const int64_t n = (int64_t)tn * 128 + quad * 32 + lane;
+                                if (g.bias && n < g.N) bias[i] = to_f<T>(((const T*)g.bias)[n]);
+                                if (g.res && n < g.N) {
+                                    const O* res = (const O*)g.res + (t0 + c) * g.ld_res + n;
+                                    add[i][0] = to_f<O>(res[0]);
+                                    if (c + 1 < valid) add[i][1] = to_f<O>(res[g.ld_res]);
+                                }
+                            }
+                            const uint32_t at = ring + (uint32_t)(c * 128 + quad * 32 + lane) * 4;
 #pragma unroll
-                        for (int s = 1; s < S; ++s) v[0] += part[s][0], v[1] += part[s][1];
-                        float bias = 0.f;
-                        if constexpr (EPI == EPI_LINEAR) {
-                            const int64_t n = (int64_t)tn * 128 + quad * 32 + lane;
-                            if (g.bias && n < g.N) bias = to_f<T>(((const T*)g.bias)[n]);
+                            for (int s = 0; s < S; ++s) {
+                                const uint32_t ra = map_rank(at, s);
+                                part[i][s][0] = ld_cluster_f32(ra);
+                                part[i][s][1] = ld_cluster_f32(ra + 512);
+                            }
                         }
-                        w.quad = quad;
-                        emit_act<EPI, 2, T, O>(g, w, v, tn, t0 + c, bias, second);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int u = u0 + i * 8 * S;
+                            if (u >= 4 * pairs) break;
+                            float v[2] = {part[i][0][0], part[i][0][1]};
+#pragma unroll
+                            for (int s = 1; s < S; ++s) v[0] += part[i][s][0], v[1] += part[i][s][1];
+                            w.quad = u & 3;
+                            emit_act<EPI, LAY, 2, T, O>(g, w, v, tn, t0 + (u >> 2) * 2, bias[i], second, add[i]);
+                        }
                     }
                 };
                 if (g.splits == 2) join(std::integral_constant<int, 2>{});
@@ -627,6 +644,169 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == 9) tmem_free<1>(tmem, cols);
+}
+
+// ------------------------------------------------------------------ a few tokens
+// One to four tokens against weights whose rows run over k: a warp takes a row (the gated block: the
+// gate and the up row of a feature) or, when rows are few, two, four or eight warps share it; each
+// lane reads 16 bytes at a time and adds in fp32; the tokens' rows come from L1. Bound by the weights' bytes; the tensor-core kernel above takes as long
+// at the memory's rate, but its start, its ring and its split cost two or three microseconds more,
+// which is half of a small call: see few_tokens().
+struct RowArgs {
+    const void *x, *w0, *w1, *bias, *res;
+    void* out;
+    int64_t ld_x, ld_w0, ld_w1, ld_res, ld_out, n;
+    int k, m, act;
+    int share;  // warps of a row
+};
+constexpr int kRowThreads = 256;
+
+// Eight values in one register quad (a load of its own: the compiler would else load them one by one).
+template <typename T>
+__device__ __forceinline__ void widen(const uint4& v, float* f) {
+    const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) Half2<T>::unpack(q[i], f[2 * i], f[2 * i + 1]);
+}
+__device__ __forceinline__ uint4 ld_kept(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint4 ld_stream(const void* p) {  // read once: not kept in L1
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ float act_any(int act, float z) {
+    switch (act) {
+        case KD_ACT_RELU: return act_fn<KD_ACT_RELU>(z);
+        case KD_ACT_SILU: return act_fn<KD_ACT_SILU>(z);
+        case KD_ACT_GELU: return act_fn<KD_ACT_GELU>(z);
+        default: return z;
+    }
+}
+
+template <int M, bool GATED, typename T, typename O>
+__global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant__ RowArgs g) {
+    constexpr int R = GATED ? 2 : 1, kBatch = GATED ? 4 : 6;  // rows of a warp, 16-byte reads of a row under way
+    grid_wait();
+    grid_release();
+    const int lane = threadIdx.x & 31;
+    __shared__ float s_sum[kRowThreads / 32][R][M];
+    const int warp = threadIdx.x >> 5, part = warp % g.share;
+    const int64_t n = ((int64_t)blockIdx.x * (kRowThreads / 32) + warp) / g.share;
+    const bool live = n < g.n;
+    const int64_t row = live ? n : g.n - 1;
+    const T* w[R];
+    w[0] = (const T*)g.w0 + row * g.ld_w0;
+    if constexpr (GATED) w[1] = (const T*)g.w1 + row * g.ld_w1;
+    const T* x = (const T*)g.x;
+    float acc[R][M];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int t = 0; t < M; ++t) acc[r][t] = 0.f;
+    const int whole = g.k & ~7;
+    const int hop = 256 * g.share;
+    for (int k0 = (part * 32 + lane) * 8; k0 < whole; k0 += hop * kBatch) {
+        uint4 v[kBatch][R];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                v[b][r] = k0 + hop * b < whole ? ld_stream(w[r] + k0 + hop * b) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int k = k0 + hop * b;
+            if (k >= whole) break;
+            float a[R][8];
+#pragma unroll
+            for (int r = 0; r < R; ++r) widen<T>(v[b][r], a[r]);
+#pragma unroll
+            for (int t = 0; t < M; ++t) {
+                if (t >= g.m) break;
+                float f[8];
+                widen<T>(ld_kept(x + t * g.ld_x + k), f);
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) acc[r][t] = fmaf(a[r][i], f[i], acc[r][t]);
+            }
+        }
+    }
+    if (part == 0 && whole + lane < g.k) {  // the last elements of a k that is no multiple of 8
+#pragma unroll
+        for (int t = 0; t < M; ++t)
+            if (t < g.m)
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    acc[r][t] = fmaf(to_f<T>(w[r][whole + lane]), to_f<T>(x[t * g.ld_x + whole + lane]), acc[r][t]);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int t = 0; t < M; ++t)
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) acc[r][t] += __shfl_xor_sync(0xffffffffu, acc[r][t], o);
+    if (g.share > 1) {  // a row's first warp adds up, in the order of the warps
+        if (lane == 0)
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int t = 0; t < M; ++t) s_sum[warp][r][t] = acc[r][t];
+        __syncthreads();
+        if (part != 0) return;
+        for (int p = 1; p < g.share; ++p)
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int t = 0; t < M; ++t) acc[r][t] += s_sum[warp + p][r][t];
+    }
+    if (!live) return;
+#pragma unroll
+    for (int t = 0; t < M; ++t) {  // lane t writes token t
+        if (lane != t || t >= g.m) continue;
+        O* out = (O*)g.out + t * g.ld_out + n;
+        if constexpr (GATED) {
+            *out = from_f<O>(act_any(g.act, acc[0][t]) * acc[R - 1][t]);
+        } else {
+            const float b = g.bias ? to_f<T>(((const T*)g.bias)[n]) : 0.f;
+            const float r = g.res ? to_f<O>(((const O*)g.res)[t * g.ld_res + n]) : 0.f;
+            *out = from_f<O>(act_any(g.act, acc[0][t] + b) + r);
+        }
+    }
+}
+
+template <bool GATED, typename T, typename O>
+int run_rows(RowArgs g, cudaStream_t stream) {
+    // sixteen warps for every SM, as long as a warp of a row still reads its batch
+    g.share = 1;
+    while (g.share < 8 && g.n * g.share < 148 * 16 && g.k >= 256 * 2 * g.share) g.share *= 2;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((g.n * g.share + kRowThreads / 32 - 1) / (kRowThreads / 32)));
+    cfg.blockDim = dim3(kRowThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    cudaError_t e;
+    if (g.m == 1) e = cudaLaunchKernelEx(&cfg, row_kernel<1, GATED, T, O>, g);
+    else if (g.m == 2) e = cudaLaunchKernelEx(&cfg, row_kernel<2, GATED, T, O>, g);
+    else e = cudaLaunchKernelEx(&cfg, row_kernel<4, GATED, T, O>, g);
+    if (e != cudaSuccess) return op_fail(KD_ECUDA, "launch failed: %s", cudaGetErrorString(e));
+    return KD_OK;
+}
+
+// Whether the row kernel is the quicker one (rows: weight matrices, 1 or 2). One token: at every size
+// measured (us, row kernel and tensor cores: 64 x 64 1.7 / 3.8, 1,536 x 1,536 3.1 / 5.2, 4,096 x 4,096 9.6
+// / 10.5, 128,256 x 4,096 151 / 160). A further token costs it a read and eight products for every 16
+// bytes of weights, and the tensor cores nothing: two tokens 2,048 x 2,048 4.6 / 5.6, 1,536 x 4,096 6.8 /
+// 6.1; four 1,536 x 1,536 5.2 / 5.4, 2,048 x 2,048 6.0 / 5.7.
+bool few_tokens(int64_t m, int64_t n, int64_t k, int rows) {
+    return m == 1 || (m <= 4 && (double)m * n * k * rows <= 9.5e6);
 }
 
 // ------------------------------------------------------------------ launch
@@ -790,7 +970,8 @@ int run_typed(GemmArgs g, int dtype, const Operand* a, const Operand* b, int pai
         if (two && (rc = make_map_out(&m[5], out_type, out[1], g.N, g.M, ld[1], gated ? 16 : 32, rows))) return rc;
     }
     if constexpr (EPI == EPI_LINEAR) {
-        if (b[0].mn) return launch<EPI, LAY_MM, T, O>(m, g, p.grid, stream);
+        if constexpr (sizeof(O) == 2)  // the weights' gradients
+            if (b[0].mn) return launch<EPI, LAY_MM, T, O>(m, g, p.grid, stream);
         if (a[0].mn) return launch<EPI, LAY_MK, T, O>(m, g, p.grid, stream);
     }
     return launch<EPI, LAY_KK, T, O>(m, g, p.grid, stream);
@@ -886,6 +1067,13 @@ int kd_linear(const kd_linear_args* p, void* stream) {
     if (q.bias && (uintptr_t)q.bias % 2) return op_fail(KD_EINVAL, "kd_linear: bias: misaligned pointer");
     if (q.residual && (rc = check_rows("kd_linear: residual", q.residual, oe, q.m, q.n, q.ld_residual))) return rc;
     if ((rc = check_rows("kd_linear: out", q.out, oe, q.m, q.n, q.ld_out))) return rc;
+    if (few_tokens(q.m, q.n, q.k, 1) && !q.w_transposed) {
+        const RowArgs r{q.x, q.w, nullptr, q.bias, q.residual, q.out, q.ld_x, q.ld_w, 0, q.ld_residual, q.ld_out, q.n, (int)q.k, (int)q.m, q.act};
+        cudaStream_t s = (cudaStream_t)stream;
+        if (q.dtype == KD_BF16)
+            return q.out_dtype == KD_F32 ? run_rows<false, __nv_bfloat16, float>(r, s) : run_rows<false, __nv_bfloat16, __nv_bfloat16>(r, s);
+        return q.out_dtype == KD_F32 ? run_rows<false, __half, float>(r, s) : run_rows<false, __half, __half>(r, s);
+    }
     GemmArgs g{};
     g.N = q.n, g.M = q.m, g.act = q.act;
     g.bias = q.bias, g.res = q.residual, g.ld_res = q.ld_residual, g.out = q.out, g.ld_out = q.ld_out;
@@ -908,6 +1096,11 @@ int kd_gated_ffn(const kd_gated_args* p, void* h, int64_t ld_h, void* stream) {
     int rc = check_gated("kd_gated_ffn", &q);
     if (rc || q.m == 0 || q.f == 0) return rc;
     if ((rc = check_rows("kd_gated_ffn: h", h, 2, q.m, q.f, ld_h))) return rc;
+    if (few_tokens(q.m, q.f, q.d, 2)) {
+        const RowArgs r{q.x, q.wg, q.wu, nullptr, nullptr, h, q.ld_x, q.ld_wg, q.ld_wu, 0, ld_h, q.f, (int)q.d, (int)q.m, q.act};
+        return q.dtype == KD_BF16 ? run_rows<true, __nv_bfloat16, __nv_bfloat16>(r, (cudaStream_t)stream)
+                                  : run_rows<true, __half, __half>(r, (cudaStream_t)stream);
+    }
     GemmArgs g{};
     g.N = q.f, g.M = q.m, g.act = q.act, g.out = h, g.ld_out = ld_h;
     const Operand a[2] = {{q.wg, q.ld_wg, false}, {q.wu, q.ld_wu, false}}, b{q.x, q.ld_x, false};

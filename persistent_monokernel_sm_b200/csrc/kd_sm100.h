@@ -268,6 +268,10 @@ template <typename T> struct Half2;
 template <> struct Half2<__nv_bfloat16> {
     static __device__ __forceinline__ float up(__nv_bfloat16 v) { return __bfloat162float(v); }
     static __device__ __forceinline__ __nv_bfloat16 down(float v) { return __float2bfloat16_rn(v); }
+    static __device__ __forceinline__ void unpack(uint32_t v, float& lo, float& hi) {
+        lo = __uint_as_float(v << 16);
+        hi = __uint_as_float(v & 0xffff0000u);
+    }
     static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
         __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
         return *reinterpret_cast<uint32_t*>(&p);
@@ -276,6 +280,10 @@ template <> struct Half2<__nv_bfloat16> {
 template <> struct Half2<__half> {
     static __device__ __forceinline__ float up(__half v) { return __half2float(v); }
     static __device__ __forceinline__ __half down(float v) { return __float2half_rn(v); }
+    static __device__ __forceinline__ void unpack(uint32_t v, float& lo, float& hi) {
+        const float2 f = __half22float2(*reinterpret_cast<__half2*>(&v));
+        lo = f.x, hi = f.y;
+    }
     static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
         __half2 p = __floats2half2_rn(lo, hi);
         return *reinterpret_cast<uint32_t*>(&p);

@@ -102,3 +102,11 @@ def test_backward_activations(act):
 def test_many_tiles():
     check_forward(1500, 512, 3000)
     check_backward(1500, 512, 3000)
+
+
+@pytest.mark.parametrize("m", [1, 2, 3, 4, 5])
+@pytest.mark.parametrize("d,f", [(8, 1), (9, 7), (515, 100), (256, 3000), (9000, 130)])
+def test_few_tokens(m, d, f):
+    check_forward(m, d, f, act="gelu")
+    check_forward(m, d, f, HF, extra=8)
+    check_forward(m, d, f, interleaved=True)

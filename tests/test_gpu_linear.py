@@ -56,3 +56,13 @@ def test_types_and_epilogues(dt, out, act, m):
 def test_many_tiles(m, n, k):
     check(m, n, k, bias=True, act="silu", extra=8)
     check(m, n, k, out=F32, w_t=True, res=True)
+
+
+@pytest.mark.parametrize("m", [1, 2, 3, 4, 5])
+@pytest.mark.parametrize("n,k", [(1, 1), (7, 9), (64, 64), (100, 515), (2400, 256), (1000, 1000), (300, 9000), (3, 20000)])
+def test_few_tokens(m, n, k):
+    """Either side of the rule between the two kernels, a row of weights per warp and shared by several,
+    lengths that are no multiple of 8."""
+    check(m, n, k, bias=True, act="gelu", res=True)
+    check(m, n, k, HF, out=F32, res=True, extra=8)
+    check(m, n, k, HF)
