@@ -12,14 +12,21 @@
 // (128 x hd fp32) in tensor memory; while one does its softmax the tensor cores work for the
 // other. For prompts the streams are two neighbouring tiles that share every key and value
 // block. With few tiles they share one tile and take alternate blocks, and the blocks are
-// split over the CTAs of a cluster besides; the partial (m, l, o) are then joined through
-// (distributed) shared memory in a fixed order.
+// split over several CTAs besides: the partial (m, l, o) of the streams are joined in shared
+// memory, those of the CTAs through a workspace by join_kernel, in a fixed order.
 //
 // Per block and stream: S = Q K^T; p = 2^(s - m) in 16 bits written over S; O += P V with P
 // read from tensor memory. A row's reference m is raised (and O rescaled) only when its maximum
 // has grown by more than 2^8: p then stays within 2^8 and O within range of fp32.
 // p is rounded to 16 bits as an operand of the second product (off by half a step of its type,
 // averaged over the row); its sum l is taken in fp32 before that rounding.
+//
+// What bounds it: for prompts the chain softmax -> P V -> next Q K^T of a stream, 2,900 clocks a
+// pair of blocks where the products alone take 2,048 and the exponentials 2,048 (4,096 tokens, 32/8
+// heads of 128: 122 us, 1.13 PFLOP/s; 16,384: 1.31). A polynomial for a part of the exponentials
+// made it longer (2/8 of them: 130 -> 137 us): the FMA pipe has no room either. One token: HBM and
+// a fixed 8 us of start, last block and join (32,768 positions, 16/8 heads: 31 us, 4.3 TB/s; 131,072:
+// 88 us, 6.1 TB/s).
 #include <cuda.h>
 #include <cuda_runtime.h>
 

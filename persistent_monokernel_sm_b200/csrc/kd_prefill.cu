@@ -225,6 +225,7 @@ int kd_prefill(kd_ctx* c, const int32_t* d_tokens, int32_t n_tokens, int32_t kv_
             t.scale = 1.f / sqrtf((float)d.hd);
             t.workspace = base + sp.part, t.workspace_bytes = sp.total - sp.part;
             if ((rc = op(kd_prompt_attention(&t, s)))) return rc;
+            if (kd_prompt_attention_workspace(&t) > 0) kd_internal_count_launch(c);  // and its join
             a = kd_linear_args{};  // x += att wo^T
             a.dtype = KD_BF16, a.out_dtype = KD_F32, a.w_transposed = 1;
             a.m = m, a.n = d.d, a.k = d.qd;

@@ -189,6 +189,51 @@ def test_offsets_past_32_bits():
         assert torch.equal(y[i], w[:, 0])
 
 
+def test_gradients_one_by_one():
+    """A NULL output is skipped; the others are what the whole call gives."""
+    g = gen(7)
+    m, d, f = 70, 128, 200
+    x, wg, wu = rows(g, m, d, 1.0, BF, "cuda"), rows(g, f, d, 0.1, BF, "cuda"), rows(g, f, d, 0.1, BF, "cuda")
+    dh = rows(g, m, f, 1.0, BF, "cuda", pad=1)
+    want = kd.gated_ffn_backward(x, wg, wu, dh)
+    args = kd.kd_gated_args(0, 2, m, d, f, x.data_ptr(), x.stride(0), wg.data_ptr(), wg.stride(0), wu.data_ptr(), wu.stride(0))
+    n = kd.kd_gated_ffn_backward_workspace(m, f)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")  # its contents do not matter
+    stream = torch.cuda.current_stream().cuda_stream
+    for mask in range(8):
+        out = [torch.full((r, d + 8), 7.0, dtype=BF, device="cuda") for r in (m, f, f)]
+        p = [o.data_ptr() if mask >> i & 1 else None for i, o in enumerate(out)]
+        kd.kd_gated_ffn_backward(args, dh.data_ptr(), f, p[0], d + 8, p[1], d + 8, p[2], d + 8, ws.data_ptr(), n, stream)
+        for i in range(3):
+            assert torch.equal(out[i][:, :d], want[i]) if mask >> i & 1 else bool((out[i] == 7.0).all())
+            assert bool((out[i][:, d:] == 7.0).all())
+
+
+FIRST_CALL = """
+import torch
+import persistent_monokernel_sm_b200 as kd
+torch.cuda.init()
+z = lambda *s: torch.ones(s, dtype=torch.bfloat16, device="cuda")
+x, x1, w, dh, q, k = z(40, 512), z(1, 512), z(64, 512), z(40, 64), z(2, 4, 64), z(2, 2000, 64)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    outs = [kd.linear(x, w), kd.linear(x1, w), kd.gated_ffn(x, w, w), *kd.gated_ffn_backward(x, w, w, dh), kd.prompt_attention(q, k, k, 1990)]
+g.replay()
+torch.cuda.synchronize()
+assert float(outs[0][0, 0]) == 512 and float(outs[1][0, 0]) == 512 and float(outs[-1][0, 0, 0]) == 1
+print("captured")
+"""
+
+
+def test_the_first_call_may_be_a_captured_one():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
 def test_gradients_against_differences():
     """The gradients' projection on a direction against central differences of sum(dh * h) in 64 bits.
     The kernels' gradients are within 2 half-steps of theirs (rounding of dg, du and the result), so a

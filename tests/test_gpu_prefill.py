@@ -85,7 +85,8 @@ def run(w, W, tokens, prefix=None, max_piece=4096, spare=3):
     launches = dec.info().launches
     dec.prefill(tokens, p, max_piece)
     assert dec.position() == p + n - 1
-    assert dec.info().launches == launches + (8 * dims["n_layers"] - 5) * -(-(n - 1) // max_piece)
+    pieces, least = -(-(n - 1) // max_piece), 8 * dims["n_layers"] - 5  # and a join where attention is split
+    assert least * pieces <= dec.info().launches - launches <= (least + dims["n_layers"] - 1) * pieces
     before = [cache_rows(dec, dims, l, s, p, p + n - 1, cap).clone() for l in range(dims["n_layers"]) for s in (0, 1)]
     _, lg = dec.decode(1, logits=True)
     dec.sync()
