@@ -575,13 +575,15 @@ Cut cut_of(int64_t n, int64_t kv_len, int r, int hkv, int hd) {
     const int64_t pair_waves = (pairs + kCtas - 1) / kCtas, unit_waves = (units + kCtas - 1) / kCtas;
     if (units <= kCtas || (kv_len >= n && pair_waves <= 4 && unit_waves < 2 * pair_waves)) {
         // One tile per CTA; few tiles' blocks go to as many CTAs as there are SMs while each of its
-        // streams keeps a block (one token behind 2,000, 16/8 heads: whole 16.6 us, by eight 9.9; one
+        // streams keeps a block, or of a short cache the CTA one (77 tokens behind 1,001, 4/2 heads of 64: by
+        // four 10.8 us, by nine 9.3; one token behind 2,000, 16/8 heads: whole 16.6, by eight 9.9; one
         // behind 32,768: by eight 37, by eighteen 31). Past sixteen, a CTA keeps six blocks: the join
         // reads every share (one token behind 32,768, 8/1 heads: by 36 19 us, by 128 28).
         c.shared = 1;
         int64_t most = blocks / 6 > 16 ? blocks / 6 : 16;
         if (most > kCtas / units) most = kCtas / units;
-        c.splits = (int)(most < blocks / 2 ? most : blocks / 2);
+        const int64_t worth = blocks <= 10 ? blocks : blocks / 2;
+        c.splits = (int)(most < worth ? most : worth);
         if (c.splits < 1) c.splits = 1;
         c.grid = units * c.splits;
         if (c.splits > 1) c.bytes = c.grid * 128 * (hd + 4) * 4 + 256;

@@ -164,6 +164,9 @@ struct GemmArgs {
     void* out2;  // the backward pass's du; the second of two products of one A (t_half > 0)
     int64_t ld_out, ld_out2;
     int tma_out;  // outputs by TMA (aligned rows), else from the lanes
+    // This launch needs nothing of the one before it, only of those before that, which that one has
+    // waited for: it starts beside it, and waits for its end before its own.
+    int beside;
     int t_half;  // token tiles of the first of two products with the same A; 0: one product
 };
 
@@ -385,7 +388,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     volatile int* dead = &s_dead;
     // What came before on the stream may still run until here; the next launch may start its own
     // set-up as this one's CTAs end.
-    grid_wait();
+    if (!g.beside) grid_wait();
     grid_release();
 
     const int rank = g.splits > 1 ? (int)cluster_rank() : 0;
@@ -643,9 +646,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             __syncwarp();
             cluster_sync_all();
         }
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // its outputs are out
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the stage has been read
         __syncwarp();
     }
+    if (g.beside) grid_wait();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1162,6 +1166,7 @@ int kd_gated_ffn_backward(const kd_gated_args* p, const void* dh, int64_t ld_dh,
         g.N = q.d, g.M = q.f;
         g.out = dwg ? dwg : dwu, g.ld_out = dwg ? ld_dwg : ld_dwu;
         g.out2 = dwu, g.ld_out2 = ld_dwu;
+        g.beside = dx != nullptr;
         if ((rc = run<EPI_LINEAR>(g, q.dtype, q.dtype, &a, b, dwg && dwu ? -1 : 1, q.m, s))) return rc;
     }
     return KD_OK;
