@@ -828,7 +828,7 @@ struct Operand {
 
 // Tile width (tokens) and split of the reduction, by an estimate of the time in microseconds.
 // A k-block costs an SM what its instructions or its product take (measured from one-tile
-// runs: 0.20 us up to 64 columns, 0.28 at 128, 0.41 at 256), or what the CTAs' loads take at the
+// runs: 0.20 us up to 64 columns, 0.28 at 128, 0.41 at 256, about linear between), or what the CTAs' loads take at the
 // 10.5 TB/s that L2 was seen to deliver to such tiles, whichever is more; a tile's epilogue runs
 // beside the next tile's products; a split costs its exchange. Both sides, measured (us):
 // 128 x 4,096 x 2,048: 32 columns 14.1, 128 columns split by four 15.5; 128 x 1,536 x 4,096: 16
@@ -839,14 +839,16 @@ struct Plan {
 
 // room[s]: clusters of s CTAs that the device runs at once (a GPU processing cluster holds whole ones:
 // fewer than sms / s; 128 CTAs in clusters of eight take two rounds).
-Plan make_plan(int64_t n_tiles, int64_t M, int kb, int sms, const int* room, int min_bn) {
+// Widths are multiples of 32 (of 64 where the tokens are the contiguous index of B), so that 257
+// tokens, say, are two tiles of 160 (257 x 6,290 x 9,142: 72 us, as three of 128 or two of 256 101).
+Plan make_plan(int64_t n_tiles, int64_t M, int kb, int sms, const int* room, bool b_mn) {
     Plan best{};
     double best_cost = 1e300;
-    for (int bn = min_bn; bn <= 256; bn *= 2) {
+    for (int bn = b_mn ? 64 : 16; bn <= 256; bn = bn < 32 ? 32 : bn + (b_mn ? 64 : 32)) {
         const int64_t tiles = n_tiles * ((M + bn - 1) / bn);
         for (int s = 1; s <= 8; s *= 2) {
             if (s > 1 && (2 * s > kb || tiles > room[s])) break;
-            const double work = bn <= 64 ? 0.20 + bn * 0.0003 : bn == 128 ? 0.28 : 0.41;
+            const double work = bn <= 64 ? 0.20 + bn * 0.0003 : 0.155 + bn * 0.001;
             const double ctas = (double)(tiles * s < sms ? tiles * s : sms);
             const double load = ctas * (kABytes + 128.0 * bn) / 10.5e6;
             const double body = (double)((kb + s - 1) / s) * (work > load ? work : load), tail = 0.4 + 0.012 * bn;
@@ -941,7 +943,7 @@ int run_typed(GemmArgs g, int dtype, const Operand* a, const Operand* b, int pai
     const int per = gated ? 64 : 128;
     const int64_t n_tiles = (g.N + per - 1) / per;
     const int64_t kblocks = (k + kBK - 1) / kBK;
-    const Plan p = make_plan(both ? 2 * n_tiles : n_tiles, g.M, (int)kblocks * (gated ? 1 : pairs), sms, room, b[0].mn ? 64 : 16);
+    const Plan p = make_plan(both ? 2 * n_tiles : n_tiles, g.M, (int)kblocks * (gated ? 1 : pairs), sms, room, b[0].mn);
     g.kb0 = (int)kblocks;
     g.kb = (int)kblocks * (gated ? 1 : pairs);
     int64_t t_tiles = (g.M + p.bn - 1) / p.bn;

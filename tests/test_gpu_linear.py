@@ -66,3 +66,11 @@ def test_few_tokens(m, n, k):
     check(m, n, k, bias=True, act="gelu", res=True)
     check(m, n, k, HF, out=F32, res=True, extra=8)
     check(m, n, k, HF)
+
+
+@pytest.mark.parametrize("m", [65, 90, 97, 150, 161, 190, 193, 220, 225, 257, 290])
+def test_widths_between_the_powers_of_two(m):
+    """Token counts that the plan cuts into tiles of 96, 160, 192 or 224 columns."""
+    check(m, 19000, 128, bias=True, act="relu")
+    check(m, 5000, 1200, out=F32, res=True)
+    check(m, 700, 2400, w_t=True, out=F32)
