@@ -316,8 +316,9 @@ typedef struct kd_attention_args {
 size_t kd_prompt_attention_workspace(const kd_attention_args *args);
 int kd_prompt_attention(const kd_attention_args *args, void *stream);
 
-/* Wait for `stream` and report a device-side wait of an operator that ran out of its limit
- * (2 s; such a kernel ends early and its outputs are not valid): KD_OK or KD_ETIMEOUT, once. */
+/* Wait for `stream` and report whether a device-side wait of an operator has run out of its limit
+ * (about 2 s; such a kernel ends early and its outputs are not valid) on the current device, in
+ * whatever call, since the last report: KD_ETIMEOUT, else KD_OK. */
 int kd_op_sync(void *stream);
 
 /* The text of the calling thread's last operator call that failed. */

@@ -24,7 +24,8 @@
 // What bounds it: for prompts the chain softmax -> P V -> next Q K^T of a stream, 2,900 clocks a
 // pair of blocks where the products alone take 2,048 and the exponentials 2,048 (4,096 tokens, 32/8
 // heads of 128: 122 us, 1.13 PFLOP/s; 16,384: 1.31). A polynomial for a part of the exponentials
-// made it longer (2/8 of them: 130 -> 137 us): the FMA pipe has no room either. One token: HBM and
+// made it longer (2/8 of them: 130 -> 137 us): the FMA pipe has no room either; so did two threads a
+// row (121 -> 139 us): the exponentials' unit is what a stream's softmax takes. One token: HBM and
 // a fixed 8 us of start, last block and join (32,768 positions, 16/8 heads: 31 us, 4.3 TB/s; 131,072:
 // 88 us, 6.1 TB/s).
 #include <cuda.h>
