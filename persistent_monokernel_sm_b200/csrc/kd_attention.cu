@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kThr, 1)
         tma_prefetch(&mk);
         tma_prefetch(&mv);
     }
-    if (warp == 9) tmem_alloc<1>(smem_u32(&s_tmem), 512);
+    if (warp == 9) tmem_alloc(smem_u32(&s_tmem), 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kThr, 1)
 #pragma unroll
                 for (int ks = 0; ks < HD / 16; ++ks) {
                     const uint32_t off = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
-                    mma_ss<1>(tmem + s * 128, qd + off, kd + off, idesc_s, ks > 0);
+                    mma_ss(tmem + s * 128, qd + off, kd + off, idesc_s, ks > 0);
                 }
                 tc_commit(sbar + 8 * s);
             };
@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(kThr, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 9) tmem_free<1>(tmem, 512);
+    if (warp == 9) tmem_free(tmem, 512);
 }
 
 // Joins the partial rows of split tiles: a warp per row, which reads eight partials at a time.

@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         tma_prefetch(&a0);
         tma_prefetch(&b0);
     }
-    if (warp == 9) tmem_alloc<1>(smem_u32(&s_tmem), cols);
+    if (warp == 9) tmem_alloc(smem_u32(&s_tmem), cols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -441,19 +441,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         if constexpr (EPI != EPI_LINEAR) {
 #pragma unroll
                             for (int q = 0; q < 4; ++q) {
-                                tma_2d<1>(sa + q * 4096, &a0, k, an + q * 16, here);
-                                tma_2d<1>(sa + q * 4096 + 2048, &a1, k, an + q * 16, here);
+                                tma_2d(sa + q * 4096, &a0, k, an + q * 16, here);
+                                tma_2d(sa + q * 4096 + 2048, &a1, k, an + q * 16, here);
                             }
                         } else if constexpr (kAMn) {
-                            tma_2d<1>(sa, ma, an, k, here);
-                            tma_2d<1>(sa + kABytes / 2, ma, an + 64, k, here);
+                            tma_2d(sa, ma, an, k, here);
+                            tma_2d(sa + kABytes / 2, ma, an + 64, k, here);
                         } else {
-                            tma_2d<1>(sa, ma, k, an, here);
+                            tma_2d(sa, ma, k, an, here);
                         }
                         if constexpr (kBMn) {
-                            for (int j = 0; j < bn; j += 64) tma_2d<1>(sb + j * 128, mb, bt + j, k, here);
+                            for (int j = 0; j < bn; j += 64) tma_2d(sb + j * 128, mb, bt + j, k, here);
                         } else {
-                            tma_2d<1>(sb, mb, k, bt, here);
+                            tma_2d(sb, mb, k, bt, here);
                         }
                         ++used;
                     }
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     ready = mbar_test(bar, ph);
 #pragma unroll
                     for (int ks = 0; ks < kBK / 16; ++ks) {
-                        mma_ss<1>(d, da + ks * kAStep, db + ks * kBStep, idesc, add);
+                        mma_ss(d, da + ks * kAStep, db + ks * kBStep, idesc, add);
                         add = true;
                     }
                     tc_commit(done);
@@ -653,7 +653,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 9) tmem_free<1>(tmem, cols);
+    if (warp == 9) tmem_free(tmem, cols);
 }
 
 // ------------------------------------------------------------------ a few tokens
