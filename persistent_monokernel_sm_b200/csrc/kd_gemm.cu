@@ -13,14 +13,15 @@
 // Structure: one CTA per SM loops over output tiles. A producer thread fills a ring of 64-deep
 // k-blocks by TMA (128-byte swizzle), one thread issues tcgen05.mma, eight warps read the
 // accumulators out of tensor memory, which holds two tiles so that the products of the next one
-// run meanwhile, and write the output through shared memory by TMA. With few tiles the reduction
+// run meanwhile, and write the output through shared memory by TMA. Wide tiles are done by two
+// CTAs at once (cta_group::2: 256 features, each CTA loads half of the tokens' operand). With few tiles the reduction
 // is split over the CTAs of a cluster, whose partial tiles are summed in rank order through
 // distributed shared memory: no workspace, one launch, the same result every time. One to four
 // tokens against a weight with rows over k go to row_kernel, without the tensor cores.
 //
 // What bounds it: with many tokens the tensor cores (4,096 x 14,336 x 4,096 with both gated
-// projections: 642 us alone, 1.50 of the measured 1.63 PFLOP/s; in a loop of seconds the power cap,
-// 772 us); with one token HBM (128,256 x 4,096: 151 us, 7.0 TB/s); between them what a tile costs
+// projections: 596 us alone, 1.61 of the measured 1.63 PFLOP/s; in a loop of seconds the power cap,
+// 714 us, 1.35 of 1.38); with one token HBM (128,256 x 4,096: 151 us, 7.0 TB/s); between them what a tile costs
 // besides its products: start, ring fill, epilogue, exchange, 3.7 us for the smallest call.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -136,6 +137,10 @@ constexpr int kChunk = 8;  // 64-deep k-blocks
 constexpr int kBK = 64;            // k-block: 128 bytes of a row
 constexpr int kABytes = 128 * kBK * 2;
 constexpr int kMaxRing = 12;
+// Columns of a tile from which CTAs work in pairs (us, single CTAs and pairs, in a loop of seconds): 256
+// columns, the gated block of 4,096 x 4,096 x 14,336 758 / 714, 500 x 2,048 x 8,192 40.1 / 37.9; 128 columns,
+// 1,024 x 2,048 x 2,048 13.2 / 13.8.
+constexpr int kPairMin = 192;
 constexpr int kRingBytes = 192 * 1024;
 // Behind the ring: 4 KB for each epilogue warp, two halves in turn, from which TMA writes the
 // output. A column of the accumulator is then one store to shared memory, with no address to
@@ -347,7 +352,7 @@ __device__ __forceinline__ void emit_act(const GemmArgs& g, Out& w, const float*
 }
 
 // ------------------------------------------------------------------ the kernel
-template <int EPI, int LAY, typename T, typename O>
+template <int CG, int EPI, int LAY, typename T, typename O>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUtensorMap a1,
                 const __grid_constant__ CUtensorMap b0, const __grid_constant__ CUtensorMap b1,
@@ -363,7 +368,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     constexpr int kStep = kSums ? kChunk : 1 << 28;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t ring = (smem_u32(smem_raw) + 1023) & ~1023u;
-    const int bbytes = g.bn * kBK * 2, sbytes = kABytes + bbytes;
+    // CG 2: a pair of CTAs (rank 0 and 1 of a cluster) works on 256 features; each loads its 128 and half
+    // of the tokens, rank 0 issues the products for both, and either holds its own rows' sums.
+    const int own = g.bn / CG;  // tokens that this CTA loads
+    const int bbytes = own * kBK * 2, sbytes = kABytes + bbytes;
     const uint32_t full = smem_u32(s_full), empty = smem_u32(s_empty);
     const uint32_t tfull = smem_u32(s_tfull), tempty = smem_u32(s_tempty), drain = smem_u32(&s_drain);
     uint32_t cols = 32;
@@ -371,7 +379,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < g.stages; ++i) mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, 1);
-        for (int i = 0; i < 2; ++i) mbar_init(tfull + 8 * i, 1), mbar_init(tempty + 8 * i, 8);
+        for (int i = 0; i < 2; ++i) mbar_init(tfull + 8 * i, 1), mbar_init(tempty + 8 * i, 8 * CG);
         mbar_init(drain, 1);
         s_dead = 0;
         fence_barrier_init();
@@ -380,9 +388,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         tma_prefetch(&a0);
         tma_prefetch(&b0);
     }
-    if (warp == 9) tmem_alloc(smem_u32(&s_tmem), cols);
+    if (warp == 9) tmem_alloc<CG>(smem_u32(&s_tmem), cols);
     tc_fence_before();
-    __syncthreads();
+    if constexpr (CG == 2) cluster_sync_all();  // the barriers of both are there
+    else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
     volatile int* dead = &s_dead;
@@ -391,8 +400,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if (!g.beside) grid_wait();
     grid_release();
 
-    const int rank = g.splits > 1 ? (int)cluster_rank() : 0;
-    const int first = blockIdx.x / g.splits, step = gridDim.x / g.splits;
+    const int member = CG == 2 ? (int)cluster_rank() : 0;  // of the pair
+    const int rank = CG == 1 && g.splits > 1 ? (int)cluster_rank() : 0;
+    const int team = CG == 2 ? 2 : g.splits;  // CTAs of a tile
+    const int first = blockIdx.x / team, step = gridDim.x / team;
     const int tiles = g.n_tiles * g.t_tiles;
     const int k_lo = (int)((long long)g.kb * rank / g.splits), k_hi = (int)((long long)g.kb * (rank + 1) / g.splits);
 
@@ -403,6 +414,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const int size = min(kGroup, g.t_tiles - grp * kGroup);
         tn = in / size;
         tt = grp * kGroup + in % size;
+        if constexpr (CG == 2) tn = 2 * tn + member;
         const bool second = kBMn && g.t_half > 0 && tt >= g.t_half;
         if (second) tt -= g.t_half;
         return second;
@@ -423,7 +435,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             for (int tile = first; tile < tiles && ok; tile += step) {
                 int tn, tt;
                 const bool second = place(tile, tn, tt);
-                const int an = tn * (EPI == EPI_LINEAR ? 128 : 64), bt = tt * bn;
+                const int an = tn * (EPI == EPI_LINEAR ? 128 : 64), bt = tt * bn + member * own;
                 int kb = k_lo;
 #pragma unroll
                 for (int seg = 0; seg < 2; ++seg) {  // the first operand pair, the second
@@ -433,39 +445,43 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll 1
                     for (; kb < end && ok; ++kb, k += kBK) {
                         if (!ready && !(ok = mbar_wait(bar + to_empty, ph, dead))) break;
-                        const uint32_t here = bar, sa = at, sb = at + kABytes;
+                        const uint32_t here = CG == 2 ? map_rank(bar, 0) : bar, sa = at, sb = at + kABytes;
+                        const uint32_t bar_now = bar;
                         at += sbytes, bar += 8;
                         if (++st == stages) st = 0, ph ^= 1, at = ring, bar = full;
                         ready = mbar_test(bar + to_empty, ph);
-                        mbar_expect(here, sbytes);
+                        if (member == 0) mbar_expect(bar_now, CG * sbytes);
                         if constexpr (EPI != EPI_LINEAR) {
 #pragma unroll
                             for (int q = 0; q < 4; ++q) {
-                                tma_2d(sa + q * 4096, &a0, k, an + q * 16, here);
-                                tma_2d(sa + q * 4096 + 2048, &a1, k, an + q * 16, here);
+                                tma_2d<CG>(sa + q * 4096, &a0, k, an + q * 16, here);
+                                tma_2d<CG>(sa + q * 4096 + 2048, &a1, k, an + q * 16, here);
                             }
                         } else if constexpr (kAMn) {
-                            tma_2d(sa, ma, an, k, here);
-                            tma_2d(sa + kABytes / 2, ma, an + 64, k, here);
+                            tma_2d<CG>(sa, ma, an, k, here);
+                            tma_2d<CG>(sa + kABytes / 2, ma, an + 64, k, here);
                         } else {
-                            tma_2d(sa, ma, k, an, here);
+                            tma_2d<CG>(sa, ma, k, an, here);
                         }
                         if constexpr (kBMn) {
-                            for (int j = 0; j < bn; j += 64) tma_2d(sb + j * 128, mb, bt + j, k, here);
+                            for (int j = 0; j < own; j += 64) tma_2d<CG>(sb + j * 128, mb, bt + j, k, here);
                         } else {
-                            tma_2d(sb, mb, k, bt, here);
+                            tma_2d<CG>(sb, mb, k, bt, here);
                         }
                         ++used;
                     }
                 }
             }
-            if (!ok)  // let the copies in flight land before the CTA ends
+            if (!ok && member == 0)  // let the copies in flight land before the CTA ends
                 for (int i = used > stages ? used - stages : 0; i < used; ++i)
                     mbar_drain(full + 8 * (i % stages), (i / stages) & 1);
+            if (ok && CG == 2)  // and the pair's arrivals on this CTA's barriers
+                for (int i = used > stages ? used - stages : 0; i < used; ++i)
+                    mbar_wait(empty + 8 * (i % stages), (i / stages) & 1, dead);
         }
         __syncwarp();
       } else if (warp == 9) {  // --------------------------------------- issuer
-        if (elect_one()) {
+        if (member == 0 && elect_one()) {
             const uint64_t a_first = make_desc(ring, kAMn ? 8192 : 16, 1024);
             const uint64_t b_first = make_desc(ring + kABytes, kBMn ? 8192 : 16, 1024);
             constexpr uint32_t kAStep = kAMn ? 2048 >> 4 : 32 >> 4, kBStep = kBMn ? 2048 >> 4 : 32 >> 4;
@@ -491,15 +507,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     ready = mbar_test(bar, ph);
 #pragma unroll
                     for (int ks = 0; ks < kBK / 16; ++ks) {
-                        mma_ss(d, da + ks * kAStep, db + ks * kBStep, idesc, add);
+                        mma_ss<CG>(d, da + ks * kAStep, db + ks * kBStep, idesc, add);
                         add = true;
                     }
-                    tc_commit(done);
+                    if constexpr (CG == 2) tc_commit_pair(done);
+                    else tc_commit(done);
                 }
-                if (ok) tc_commit(tfull + 8 * buf);
+                if (ok) {
+                    if constexpr (CG == 2) tc_commit_pair(tfull + 8 * buf);
+                    else tc_commit(tfull + 8 * buf);
+                }
             }
             if (!ok) {
-                tc_commit(drain);
+                if constexpr (CG == 2) tc_commit_pair(drain);
+                else tc_commit(drain);
                 mbar_drain(drain, 0);
             }
         }
@@ -515,6 +536,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const int quad = warp & 3, half = warp >> 2;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         Out w{&o0, &o1, smem_raw + (ring - smem_u32(smem_raw)) + kRingBytes + warp * kStageBytes, 0, quad, lane};
+        auto give_back = [&](uint32_t bar) {  // to the issuer, of the pair's first CTA
+            if constexpr (CG == 2) mbar_arrive_cluster(map_rank(bar, 0));
+            else mbar_arrive(bar);
+        };
         int local = 0;
         bool ok = true;
         for (int tile = first; tile < tiles && ok; tile += step) {
@@ -567,7 +592,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     }
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(tempty + 8 * buf);
+                    if (lane == 0) give_back(tempty + 8 * buf);
                 }
                 if (!ok) break;
 #pragma unroll
@@ -587,7 +612,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(tempty + 8 * buf);
+                if (lane == 0) give_back(tempty + 8 * buf);
                 ++local;
             }
         }
@@ -651,9 +676,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     if (g.beside) grid_wait();
     tc_fence_before();
-    __syncthreads();
+    if constexpr (CG == 2) {
+        __syncwarp();
+        cluster_sync_all();  // neither leaves while the other reads its memory or arrives on its barriers
+    } else {
+        __syncthreads();
+    }
     tc_fence_after();
-    if (warp == 9) tmem_free(tmem, cols);
+    if (warp == 9) tmem_free<CG>(tmem, cols);
 }
 
 // ------------------------------------------------------------------ a few tokens
@@ -866,13 +896,13 @@ Plan make_plan(int64_t n_tiles, int64_t M, int kb, int sms, const int* room, boo
     return best;
 }
 
-template <int EPI, int LAY, typename T, typename O>
+template <int CG, int EPI, int LAY, typename T, typename O>
 int launch(const CUtensorMap* m, const GemmArgs& g, int grid, cudaStream_t stream) {
     int dev = 0;
     cudaGetDevice(&dev);
     static std::atomic<bool> ready[64];
     if (dev >= 64 || !ready[dev].load()) {
-        cudaError_t e = cudaFuncSetAttribute(gemm_kernel<EPI, LAY, T, O>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(gemm_kernel<CG, EPI, LAY, T, O>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              kSmemBytes);
         if (e != cudaSuccess) return op_fail(KD_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
         if (dev < 64) ready[dev].store(true);
@@ -886,11 +916,11 @@ int launch(const CUtensorMap* m, const GemmArgs& g, int grid, cudaStream_t strea
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = g.splits;
+    at[1].val.clusterDim.x = CG == 2 ? 2 : g.splits;
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = g.splits > 1 ? 2 : 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_kernel<EPI, LAY, T, O>, m[0], m[1], m[2], m[3], m[4], m[5], g);
+    cfg.numAttrs = CG == 2 || g.splits > 1 ? 2 : 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_kernel<CG, EPI, LAY, T, O>, m[0], m[1], m[2], m[3], m[4], m[5], g);
     if (e != cudaSuccess) return op_fail(KD_ECUDA, "launch failed: %s", cudaGetErrorString(e));
     return KD_OK;
 }
@@ -903,7 +933,7 @@ int cluster_room(int sms, int room[9]) {
     for (int i = 0, s = 2; s <= 8; ++i, s *= 2) {
         int n = dev < 64 ? cached[dev][i].load() : 0;
         if (n == 0) {
-            const auto kernel = gemm_kernel<EPI_LINEAR, LAY_KK, __nv_bfloat16, __nv_bfloat16>;
+            const auto kernel = gemm_kernel<1, EPI_LINEAR, LAY_KK, __nv_bfloat16, __nv_bfloat16>;
             e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
             cudaLaunchConfig_t cfg{};
             cfg.gridDim = dim3(sms / s * s);
@@ -949,21 +979,27 @@ int run_typed(GemmArgs g, int dtype, const Operand* a, const Operand* b, int pai
     int64_t t_tiles = (g.M + p.bn - 1) / p.bn;
     if (both) g.t_half = (int)t_tiles, t_tiles *= 2;
     if (n_tiles * t_tiles > 0x3fffffff) return op_fail(KD_EINVAL, "too many output tiles");
-    g.n_tiles = (int)n_tiles;
+    // Pairs of CTAs where they take no more rounds than single ones.
+    const int64_t pair_tiles = (n_tiles + 1) / 2 * t_tiles;
+    const bool pair = p.splits == 1 && p.bn >= kPairMin && p.bn % (b[0].mn ? 128 : 64) == 0 && n_tiles > 1 && room[2] >= sms / 2 &&
+                      (pair_tiles + sms / 2 - 1) / (sms / 2) <= (n_tiles * t_tiles + sms - 1) / sms;
+    const int cg = pair ? 2 : 1;
+    const int grid = pair ? 2 * (int)(pair_tiles < sms / 2 ? pair_tiles : sms / 2) : p.grid;
+    g.n_tiles = (int)(pair ? (n_tiles + 1) / 2 : n_tiles);
     g.t_tiles = (int)t_tiles;
     g.bn = p.bn;
     g.splits = p.splits;
-    g.stages = kRingBytes / (kABytes + p.bn * kBK * 2);
+    g.stages = kRingBytes / (kABytes + p.bn / cg * kBK * 2);
     if (g.stages > kMaxRing) g.stages = kMaxRing;
-    g.idesc = make_idesc(128, p.bn, dtype == KD_BF16, a[0].mn, b[0].mn);
+    g.idesc = make_idesc(128 * cg, p.bn, dtype == KD_BF16, a[0].mn, b[0].mn);
     CUtensorMap m[6];  // A, A of the second pair, B, the second B, the outputs
     const int a_box = gated ? 16 : 128;
     if ((rc = operand_map(&m[0], dtype, a[0], g.N, k, a_box))) return rc;
-    if ((rc = operand_map(&m[2], dtype, b[0], g.M, k, p.bn))) return rc;
+    if ((rc = operand_map(&m[2], dtype, b[0], g.M, k, p.bn / cg))) return rc;
     m[1] = m[0];
     m[3] = m[2];
     if (pairs > 1 && (rc = operand_map(&m[1], dtype, a[1], g.N, k, a_box))) return rc;
-    if ((both || (pairs > 1 && !gated)) && (rc = operand_map(&m[3], dtype, b[1], g.M, k, p.bn))) return rc;
+    if ((both || (pairs > 1 && !gated)) && (rc = operand_map(&m[3], dtype, b[1], g.M, k, p.bn / cg))) return rc;
     const bool two = both || EPI == EPI_GATED_BWD;
     const int out_type = sizeof(O) == 4 ? KD_F32 : dtype;
     if (!two) g.ld_out2 = g.ld_out, g.out2 = g.out;
@@ -983,10 +1019,10 @@ int run_typed(GemmArgs g, int dtype, const Operand* a, const Operand* b, int pai
     }
     if constexpr (EPI == EPI_LINEAR) {
         if constexpr (sizeof(O) == 2)  // the weights' gradients
-            if (b[0].mn) return launch<EPI, LAY_MM, T, O>(m, g, p.grid, stream);
-        if (a[0].mn) return launch<EPI, LAY_MK, T, O>(m, g, p.grid, stream);
+            if (b[0].mn) return pair ? launch<2, EPI, LAY_MM, T, O>(m, g, grid, stream) : launch<1, EPI, LAY_MM, T, O>(m, g, grid, stream);
+        if (a[0].mn) return pair ? launch<2, EPI, LAY_MK, T, O>(m, g, grid, stream) : launch<1, EPI, LAY_MK, T, O>(m, g, grid, stream);
     }
-    return launch<EPI, LAY_KK, T, O>(m, g, p.grid, stream);
+    return pair ? launch<2, EPI, LAY_KK, T, O>(m, g, grid, stream) : launch<1, EPI, LAY_KK, T, O>(m, g, grid, stream);
 }
 
 template <int EPI>
