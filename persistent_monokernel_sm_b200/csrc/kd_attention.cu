@@ -449,20 +449,22 @@ __global__ void __launch_bounds__(kThr, 1)
                 const int tokens = min(a.tq, a.n - tile[0] * a.tq), rows = tokens * a.r;
                 constexpr int E = HD / 32;
                 for (int row = warp; row < rows; row += 8) {
-                    const float m0 = stat[row], m1 = stat[256 + row], best = fmaxf(m0, m1);
-                    // a stream that saw nothing wrote no output
-                    const float w0 = m0 == -INFINITY ? 0.f : ex2(m0 - best), w1 = m1 == -INFINITY ? 0.f : ex2(m1 - best);
+                    const float m0 = stat[row], m1 = stat[256 + row], l0 = stat[128 + row], l1 = stat[384 + row];
+                    const float best = fmaxf(m0, m1);
+                    // A stream that saw nothing has l = 0 and may have written no output. (m does not tell: the
+                    // maximum passes over NaN, so that scores of NaN alone leave it at -infinity, and l at NaN.)
+                    const float w0 = l0 == 0.f ? 0.f : ex2(m0 - best), w1 = l1 == 0.f ? 0.f : ex2(m1 - best);
                     float l = 0.f, o[E];
                     const float *p0 = part_at(0, row) + lane * E, *p1 = part_at(1, row) + lane * E;
 #pragma unroll
                     for (int e = 0; e < E; ++e) o[e] = 0.f;
-                    if (m0 != -INFINITY) {
-                        l = w0 * stat[128 + row];
+                    if (l0 != 0.f) {
+                        l = w0 * l0;
 #pragma unroll
                         for (int e = 0; e < E; ++e) o[e] = w0 * p0[e];
                     }
-                    if (m1 != -INFINITY) {
-                        l += w1 * stat[384 + row];
+                    if (l1 != 0.f) {
+                        l += w1 * l1;
 #pragma unroll
                         for (int e = 0; e < E; ++e) o[e] = fmaf(w1, p1[e], o[e]);
                     }
@@ -485,8 +487,8 @@ __global__ void __launch_bounds__(kThr, 1)
 }
 
 // Joins the partial rows of split tiles: a warp per row, which reads eight partials at a time.
-// With m the maximum over the partials that saw anything, o = sum 2^(m_p - m) o_p / sum
-// 2^(m_p - m) l_p, in the order of p.
+// With m the maximum over the partials that saw anything (l_p is not 0; NaN counts as seen), o = sum
+// 2^(m_p - m) o_p / sum 2^(m_p - m) l_p, in the order of p.
 template <int HD, typename T>
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttnArgs a) {
     grid_wait();
@@ -515,7 +517,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttnA
         }
 #pragma unroll
         for (int p = 0; p < 8; ++p) {
-            if (p0 + p >= a.splits || m[p] == -INFINITY) continue;
+            if (p0 + p >= a.splits || s[p] == 0.f) continue;
             const float wp = ex2(m[p] - best);
             l = fmaf(wp, s[p], l);
 #pragma unroll
