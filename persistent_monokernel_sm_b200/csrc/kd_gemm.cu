@@ -90,10 +90,18 @@ static int encode(CUtensorMap* m, int dtype, const void* base, int rank, const c
     const CUtensorMapDataType type = dtype == KD_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                      : dtype == KD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    const CUresult r = f(m, type, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, ones,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    auto fill = [&]() {
+        return f(m, type, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                 swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult r = fill();
+    if (r == CUDA_ERROR_INVALID_CONTEXT) {
+        // The driver's function needs a current context, which a host thread gets with its first runtime
+        // call of some kinds; this may be the thread's first.
+        int dev = 0;
+        if (cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) r = fill();
+    }
     if (r != CUDA_SUCCESS) return op_fail(KD_ECUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
     return KD_OK;
 }
