@@ -248,7 +248,7 @@ enum { KD_ACT_NONE = 0, KD_ACT_RELU = 1, KD_ACT_SILU = 2, KD_ACT_GELU = 3 };
 /* out[m][n] = residual[m][n] + act(sum_k x[m][k] w[n][k] + bias[n]).
  * dtype: of x, w and bias (KD_BF16, KD_F16). out_dtype: of residual and out (dtype or KD_F32).
  * w_transposed: w is laid out [k][n] instead of [n][k]. bias, residual: may be NULL.
- * m and n may be 0 (nothing is done); k >= 1. */
+ * m and n may be 0 (nothing is done); k >= 1; none above 2^31 - 16384 (nor m, d, f below). */
 typedef struct kd_linear_args {
     int32_t dtype, out_dtype, act, w_transposed;
     int64_t m, n, k;

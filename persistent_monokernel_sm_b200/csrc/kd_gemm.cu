@@ -708,6 +708,10 @@ struct RowArgs {
     int share;  // warps of a row
 };
 constexpr int kRowThreads = 256;
+constexpr int kRowBatch = 6;                       // 16-byte reads of a row under way (4 of two rows)
+constexpr int kRowShare = 8;                       // warps of a row, at most
+constexpr int kRowHop = 16384;                     // elements, not less than a step over k
+static_assert(256 * kRowShare * kRowBatch <= kRowHop, "a step over k");
 
 // Eight values in one register quad (a load of its own: the compiler would else load them one by one).
 template <typename T>
@@ -737,7 +741,7 @@ __device__ __forceinline__ float act_any(int act, float z) {
 
 template <int M, bool GATED, typename T, typename O>
 __global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant__ RowArgs g) {
-    constexpr int R = GATED ? 2 : 1, kBatch = GATED ? 4 : 6;  // rows of a warp, 16-byte reads of a row under way
+    constexpr int R = GATED ? 2 : 1, kBatch = GATED ? 4 : kRowBatch;  // rows of a warp, reads of a row under way
     grid_wait();
     grid_release();
     const int lane = threadIdx.x & 31;
@@ -830,7 +834,7 @@ template <bool GATED, typename T, typename O>
 int run_rows(RowArgs g, cudaStream_t stream) {
     // sixteen warps for every SM, as long as a warp of a row still reads its batch
     g.share = 1;
-    while (g.share < 8 && g.n * g.share < 148 * 16 && g.k >= 256 * 2 * g.share) g.share *= 2;
+    while (g.share < kRowShare && g.n * g.share < 148 * 16 && g.k >= 256 * 2 * g.share) g.share *= 2;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)((g.n * g.share + kRowThreads / 32 - 1) / (kRowThreads / 32)));
     cfg.blockDim = dim3(kRowThreads);
@@ -1068,7 +1072,8 @@ int check_rows(const char* what, const void* p, int elem, int64_t rows, int64_t 
     return KD_OK;
 }
 
-constexpr int64_t kMaxDim = 0x7fffffff - 1024;  // TMA coordinates are 32-bit
+// TMA coordinates are 32-bit, and so is the row kernel's k, which steps past the end by less than a hop.
+constexpr int64_t kMaxDim = ((int64_t)1 << 31) - kRowHop;
 
 int check_sizes(const char* who, int dtype, int act, int64_t m, int64_t n, int64_t k) {
     if (dtype != KD_BF16 && dtype != KD_F16) return op_fail(KD_EINVAL, "%s: dtype must be KD_BF16 or KD_F16", who);
