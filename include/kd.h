@@ -316,9 +316,14 @@ typedef struct kd_attention_args {
 size_t kd_prompt_attention_workspace(const kd_attention_args *args);
 int kd_prompt_attention(const kd_attention_args *args, void *stream);
 
-/* Wait for `stream` and report whether a device-side wait of an operator has run out of its limit
- * (about 2 s; such a kernel ends early and its outputs are not valid) on the current device, in
- * whatever call, since the last report: KD_ETIMEOUT, else KD_OK. */
+/* Time limit, in nanoseconds (>= 1; default 2 s), of every device-side wait of the calling thread's
+ * later operator calls, counted in SM clocks at two a nanosecond: about the limit, not less. A wait that
+ * exceeds it sets the device's status and its kernel ends early (none traps, none hangs: copies and
+ * products under way are awaited under a separate fixed bound); its outputs are not valid. */
+int kd_op_set_timeout(int64_t ns);
+
+/* Wait for `stream` and report whether a device-side wait of an operator has run out of its limit on the
+ * current device, in whatever call, since the last report: KD_ETIMEOUT, else KD_OK. */
 int kd_op_sync(void *stream);
 
 /* The text of the calling thread's last operator call that failed. */

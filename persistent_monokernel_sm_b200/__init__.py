@@ -18,7 +18,7 @@ __all__ = ["KdError", "kd_config", "kd_weights", "kd_info", "load_library", "Dec
            "kd_last_error", "kd_strerror", "kd_destroy", "LIB_PATH", "ERRORS",
            "kd_linear_args", "kd_gated_args", "kd_linear", "kd_gated_ffn", "kd_gated_ffn_backward_workspace",
            "kd_gated_ffn_backward", "kd_attention_args", "kd_prompt_attention_workspace",
-           "kd_prompt_attention", "kd_op_sync", "kd_op_error",
+           "kd_prompt_attention", "kd_op_set_timeout", "kd_op_sync", "kd_op_error",
            "kd_prefill_workspace", "kd_prefill",
            "linear", "gated_ffn", "gated_ffn_backward", "prompt_attention"]
 
@@ -137,6 +137,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "kd_gated_ffn_backward": (ctypes.c_int, [ctypes.c_char_p] + [_P, ctypes.c_int64] * 4 + [_P, ctypes.c_size_t, _P]),
         "kd_prompt_attention_workspace": (ctypes.c_size_t, [ctypes.c_char_p]),
         "kd_prompt_attention": (ctypes.c_int, [ctypes.c_char_p, _P]),
+        "kd_op_set_timeout": (ctypes.c_int, [ctypes.c_int64]),
         "kd_op_sync": (ctypes.c_int, [_P]),
         "kd_op_error": (ctypes.c_char_p, []),
     }
@@ -283,6 +284,10 @@ def kd_prompt_attention_workspace(args: kd_attention_args) -> int:
 
 def kd_prompt_attention(args: kd_attention_args, stream: int | None) -> int:
     return _check_op(load_library().kd_prompt_attention(bytes(args), stream), "kd_prompt_attention")
+
+
+def kd_op_set_timeout(ns: int) -> int:
+    return _check_op(load_library().kd_op_set_timeout(ns), "kd_op_set_timeout")
 
 
 def kd_op_sync(stream: int | None) -> int:

@@ -58,6 +58,7 @@ struct AttnArgs {
     float scale_log2;
     void* out;
     int64_t out_token, out_head;
+    long long limit;  // of a wait, in SM clocks
 };
 
 template <int HD> struct Shape {
@@ -133,13 +134,14 @@ __global__ void __launch_bounds__(kThr, 1)
     __shared__ __align__(8) uint64_t s_full[kSlots], s_empty[kSlots], s_q, s_s[2], s_p[4], s_o[2], s_drain;
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_dead;
+    __shared__ int s_loads;  // the producer's, of the ring
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t qs = (smem_u32(smem_raw) + 1023) & ~1023u;
     const uint32_t ring = qs + 2 * kBlock;
     const uint32_t full = smem_u32(s_full), empty = smem_u32(s_empty), qbar = smem_u32(&s_q);
     const uint32_t sbar = smem_u32(s_s), pbar = smem_u32(s_p), obar = smem_u32(s_o), drain = smem_u32(&s_drain);
-    volatile int* dead = &s_dead;
+    const Guard dead{&s_dead, a.limit};
     // (m, l) of the two streams' rows for the join: where a second query tile would be
     float* stat = reinterpret_cast<float*>(smem_raw + (qs + kBlock - smem_u32(smem_raw)));
     auto part_at = [&](int s, int row) {  // a row's partial output, where the blocks were
@@ -202,7 +204,7 @@ __global__ void __launch_bounds__(kThr, 1)
             for (int s = 0; s < two; ++s)
                 for (int h = 0; h < kHalves; ++h)
                     tma_3d(qs + s * kBlock + h * 16384, &mq, h * 64, g * a.r, tile[s] * a.tq, qbar);
-            int it = 0, st = 0;
+            int st = 0, loads = 0;
             uint32_t ph = 1;
             bool ok = true;
             auto load = [&](const CUtensorMap* m, int block) {
@@ -211,7 +213,7 @@ __global__ void __launch_bounds__(kThr, 1)
 #pragma unroll
                 for (int h = 0; h < kHalves; ++h)
                     tma_3d(ring + st * kBlock + h * 16384, m, h * 64, (lo + block) * kKeys, g, full + 8 * st);
-                ++it;
+                ++loads;
                 if (++st == kSlots) st = 0, ph ^= 1;
             };
             for (int i = 0; i < ahead; ++i) load(&mk, i);
@@ -219,11 +221,7 @@ __global__ void __launch_bounds__(kThr, 1)
                 load(&mv, i);
                 if (i + ahead < total) load(&mk, i + ahead);
             }
-            if (!ok) {  // let the copies in flight land before the CTA ends
-                mbar_drain(qbar, 0);
-                for (int i = it > kSlots ? it - kSlots : 0; i < it; ++i)
-                    mbar_drain(full + 8 * (i % kSlots), (i / kSlots) & 1);
-            }
+            s_loads = loads;
         }
         __syncwarp();
     } else if (warp == 9) {  // --------------------------------------- issuer
@@ -237,7 +235,7 @@ __global__ void __launch_bounds__(kThr, 1)
             const int n0 = nb[0], n1 = nb[1];
             int slot = 0;
             uint32_t ph = 0;
-            bool ok = mbar_wait(qbar, 0, dead);
+            bool ok = mbar_first(qbar, 0, dead) && mbar_wait(qbar, 0, dead);
             auto take = [&]() {  // the next slot of the ring, once it is filled
                 const int at = slot;
                 ok = ok && mbar_wait(full + 8 * at, ph, dead);
@@ -306,10 +304,6 @@ __global__ void __launch_bounds__(kThr, 1)
                     tc_commit(empty + 8 * v);
                     if (k >= 0) tc_commit(empty + 8 * k);
                 }
-            }
-            if (!ok) {
-                tc_commit(drain);
-                mbar_drain(drain, 0);
             }
         }
         __syncwarp();
@@ -445,7 +439,7 @@ __global__ void __launch_bounds__(kThr, 1)
             // The two streams' partials of a row are joined by a warp, whose lanes hold HD / 32
             // neighbouring outputs each; a split tile's go to the workspace for join_kernel.
             __syncthreads();
-            if (!*dead) {
+            if (!s_dead) {
                 const int tokens = min(a.tq, a.n - tile[0] * a.tq), rows = tokens * a.r;
                 constexpr int E = HD / 32;
                 for (int row = warp; row < rows; row += 8) {
@@ -483,6 +477,20 @@ __global__ void __launch_bounds__(kThr, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (__builtin_expect(s_dead, 0)) {
+        // A wait has given up: no thread starts anything any more; products and copies under way, whichever
+        // role gave up, end before the shared and the tensor memory goes.
+        if (warp == 9 && elect_one()) {
+            tc_commit(drain);
+            mbar_drain(drain, 0);
+        }
+        if (warp == 8 && elect_one()) {
+            mbar_drain(qbar, 0);
+            for (int i = s_loads > kSlots ? s_loads - kSlots : 0; i < s_loads; ++i)
+                mbar_drain(full + 8 * (i % kSlots), (i / kSlots) & 1);
+        }
+        __syncthreads();
+    }
     if (warp == 9) tmem_free(tmem, 512);
 }
 
@@ -665,6 +673,7 @@ extern "C" int kd_prompt_attention(const kd_attention_args* p, void* stream) {
                        (size_t)c.bytes);
     a.shared = c.shared, a.splits = c.splits;
     a.parts = (float*)(((uintptr_t)q.workspace + 255) & ~(uintptr_t)255);
+    a.limit = op_limit();
     const int64_t grid = c.grid;
     const bool bf = q.dtype == KD_BF16;
     CUtensorMap mq, mk, mv;

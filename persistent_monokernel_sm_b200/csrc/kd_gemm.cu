@@ -65,6 +65,10 @@ int op_sm_count(int* sms) {
     return KD_OK;
 }
 
+// Per calling thread. SM clocks run at less than two a nanosecond.
+static thread_local long long t_limit_ns = 2000000000ll;
+long long op_limit() { return 2 * (t_limit_ns < (1ll << 61) ? t_limit_ns : 1ll << 61); }
+
 typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -181,6 +185,7 @@ struct GemmArgs {
     // waited for: it starts beside it, and waits for its end before its own.
     int beside;
     int t_half;  // token tiles of the first of two products with the same A; 0: one product
+    long long limit;  // of a wait, in SM clocks
 };
 
 // ------------------------------------------------------------------ activations
@@ -360,6 +365,28 @@ __device__ __forceinline__ void emit_act(const GemmArgs& g, Out& w, const float*
 }
 
 // ------------------------------------------------------------------ the kernel
+// Where a wait of a CTA or of its pair has given up and no thread starts anything any more, products and
+// copies may still be under way, whichever role gave up. They end before the shared and the tensor memory
+// goes: the products by a commit (on both CTAs of a pair), the copies on their barriers; of a pair, where
+// one CTA may have loaded what the other has not, by a pause. Not inlined, which
+// leaves the code out of the way: 0.1 us a launch less.
+template <int CG>
+__device__ __noinline__ void unwind_products(bool first, uint32_t drain) {
+    if (first) {
+        if constexpr (CG == 2) tc_commit_pair(drain);
+        else tc_commit(drain);
+    }
+    mbar_drain(drain, 0);
+}
+template <int CG>
+__device__ __noinline__ void unwind_loads(uint32_t full, int stages, int loads) {
+    if constexpr (CG == 2) {
+        drain_pause();
+    } else {
+        for (int i = loads > stages ? loads - stages : 0; i < loads; ++i) mbar_drain(full + 8 * (i % stages), (i / stages) & 1);
+    }
+}
+
 template <int CG, int EPI, int LAY, typename T, typename O>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUtensorMap a1,
@@ -370,6 +397,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     __shared__ __align__(8) uint64_t s_full[kMaxRing], s_empty[kMaxRing], s_tfull[2], s_tempty[2], s_drain;
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_dead;
+    __shared__ int s_loads;  // the producer's
 
     constexpr bool kAMn = LAY != LAY_KK, kBMn = LAY == LAY_MM;
     constexpr bool kSums = EPI == EPI_LINEAR && sizeof(O) == 4;  // add sums of kStep k-blocks
@@ -402,7 +430,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    volatile int* dead = &s_dead;
+    const Guard dead{&s_dead, g.limit};
     // What came before on the stream may still run until here; the next launch may start its own
     // set-up as this one's CTAs end.
     if (!g.beside) grid_wait();
@@ -428,6 +456,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         return second;
     };
 
+    auto give_up = [&]() {  // tells the other CTA of a pair
+        if constexpr (CG == 2) st_cluster_u32(map_rank(smem_u32(const_cast<int*>(&s_dead)), member ^ 1), 1);
+    };
+
     if (warp >= 8) {
       set_regs_down<kAuxRegs>();
       // The two roles run in one thread each, and at a few hundred clocks per k-block it is their
@@ -437,7 +469,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const uint32_t to_empty = empty - full;
       if (warp == 8) {  // ---------------------------------------------- producer
         if (elect_one()) {
-            int st = 0, used = 0;
+            int st = 0, loads = 0;
             uint32_t ph = 1, bar = full, at = ring;
             bool ok = true, ready = true;  // the ring starts empty
             for (int tile = first; tile < tiles && ok; tile += step) {
@@ -476,16 +508,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         } else {
                             tma_2d<CG>(sb, mb, k, bt, here);
                         }
-                        ++used;
+                        ++loads;
                     }
                 }
             }
-            if (!ok && member == 0)  // let the copies in flight land before the CTA ends
-                for (int i = used > stages ? used - stages : 0; i < used; ++i)
-                    mbar_drain(full + 8 * (i % stages), (i / stages) & 1);
-            if (ok && CG == 2)  // and the pair's arrivals on this CTA's barriers
-                for (int i = used > stages ? used - stages : 0; i < used; ++i)
-                    mbar_wait(empty + 8 * (i % stages), (i / stages) & 1, dead);
+            if (ok && CG == 2)  // the pair's arrivals on this CTA's barriers
+                for (int i = loads > stages ? loads - stages : 0; i < loads && ok; ++i)
+                    ok = mbar_wait(empty + 8 * (i % stages), (i / stages) & 1, dead);
+            s_loads = loads;
+            if (!ok) give_up();
         }
         __syncwarp();
       } else if (warp == 9) {  // --------------------------------------- issuer
@@ -496,7 +527,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const uint32_t idesc = g.idesc, hop = (uint32_t)sbytes >> 4;
             int st = 0, local = 0;  // local: accumulators so far
             uint32_t ph = 0, bar = full, off = 0;
-            bool ok = true, ready = false;
+            bool ok = first >= tiles || mbar_first(full, 0, dead), ready = false;
             for (int tile = first; tile < tiles && ok; tile += step)
               for (int kb = k_lo; kb < k_hi && ok; ++local) {
                 const int buf = local & 1, c_hi = min(k_hi, kb + kStep);
@@ -526,11 +557,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     else tc_commit(tfull + 8 * buf);
                 }
             }
-            if (!ok) {
-                if constexpr (CG == 2) tc_commit_pair(drain);
-                else tc_commit(drain);
-                mbar_drain(drain, 0);
-            }
+            if (!ok) give_up();
         }
         __syncwarp();
       }
@@ -624,10 +651,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 ++local;
             }
         }
+        if (!ok && lane == 0) give_up();
         if (g.splits > 1) {
             __syncwarp();
             cluster_sync_all();
-            if (!*dead) {
+            if (!s_dead) {
                 int tn, tt;
                 const bool second = place(first, tn, tt);
                 const int64_t t0 = (int64_t)tt * g.bn;
@@ -691,6 +719,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         __syncthreads();
     }
     tc_fence_after();
+    if (__builtin_expect(s_dead, 0)) {
+        if (warp == 9 && elect_one()) unwind_products<CG>(member == 0, drain);
+        if (warp == 8 && elect_one()) unwind_loads<CG>(full, g.stages, s_loads);
+        __syncwarp();
+        if constexpr (CG == 2) cluster_sync_all();
+        else __syncthreads();
+    }
     if (warp == 9) tmem_free<CG>(tmem, cols);
 }
 
@@ -1018,6 +1053,7 @@ int run_typed(GemmArgs g, int dtype, const Operand* a, const Operand* b, int pai
     if (EPI == EPI_GATED_BWD) g.ld_out2 = g.ld_out;
     int64_t ld[2] = {g.ld_out, g.ld_out2};
     const void* out[2] = {g.out, g.out2};
+    g.limit = op_limit();
     g.tma_out = 1;
     for (int i = 0; i < 2; ++i) {
         if (g.M == 1) ld[i] = (g.N + 7) & ~(int64_t)7;  // one row: its distance to the next is not used
@@ -1103,6 +1139,12 @@ using namespace kd;
 extern "C" {
 
 const char* kd_op_error(void) { return t_err; }
+
+int kd_op_set_timeout(int64_t ns) {
+    if (ns < 1) return op_fail(KD_EINVAL, "kd_op_set_timeout: the limit must be at least 1 ns");
+    t_limit_ns = ns;
+    return KD_OK;
+}
 
 int kd_op_sync(void* stream) {
     unsigned int a = 0, b = 0;

@@ -6,6 +6,8 @@
 #include <stdint.h>
 
 namespace kd {
+// The limit of device-side waits that the calling thread has set, in SM clocks.
+long long op_limit();
 // The status word of kd_gemm.cu / kd_attention.cu, which is cleared.
 int gemm_status(cudaStream_t s, unsigned int* st);
 int attention_status(cudaStream_t s, unsigned int* st);

@@ -15,10 +15,14 @@ namespace kd {
 // kd_op_sync reads and clears them.
 static __device__ unsigned int g_op_status;
 
-// Limits in SM clocks (about 2 s and 0.1 s at 1.9 GHz). The waits read the SM's own clock: a
-// read of the global timer costs about as much as the wait it would guard.
-constexpr long long kWaitClocks = 4000000000ll;  // of every device-side wait
-constexpr long long kDrainClocks = 200000000ll;  // of the wait for copies in flight
+// What a CTA's waits go by: its give-up flag and their limit in SM clocks. The waits read the SM's
+// own clock: a read of the global timer costs about as much as the wait it would guard.
+struct Guard {
+    volatile int* dead;
+    long long limit;
+};
+constexpr long long kSuspendClocks = 1 << 20;    // more than try_wait suspends a thread for
+constexpr long long kDrainClocks = 200000000ll;  // of the wait for copies in flight: about 0.1 s
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return (uint32_t)__cvta_generic_to_shared(p);
@@ -68,34 +72,48 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+__device__ __forceinline__ void raise_timeout(const Guard& w) {
+    *w.dead = 1;
+    atomicExch(&g_op_status, 1u);
+}
 // Waits until the phase of `parity` has completed. Gives up when the limit has passed or
 // another wait of this CTA has given up (*dead), and then returns false: the caller unwinds.
-__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int* dead) {
+__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, const Guard& w) {
     const long long t0 = clock64();
     for (;;) {
         for (int i = 0; i < 32; ++i)
             if (mbar_try(bar, parity)) return true;
-        if (*dead) return false;
-        if (clock64() - t0 > kWaitClocks) {
-            *dead = 1;
-            atomicExch(&g_op_status, 1u);
+        if (*w.dead) return false;
+        if (clock64() - t0 > w.limit) {
+            raise_timeout(w);
             return false;
         }
     }
 }
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const Guard& w) {
     if (mbar_try(bar, parity)) return true;
-    return mbar_wait_long(bar, parity, dead);
+    return mbar_wait_long(bar, parity, w);
+}
+// A first look at a kernel's first barrier: within a limit that is shorter than a thread may be suspended for,
+// it gives up at once unless the phase has completed.
+__device__ __forceinline__ bool mbar_first(uint32_t bar, uint32_t parity, const Guard& w) {
+    if (__builtin_expect(w.limit >= kSuspendClocks, 1) || mbar_test(bar, parity)) return true;
+    raise_timeout(w);
+    return false;
 }
 // The same by all lanes of a warp, with one answer.
-__device__ __forceinline__ bool mbar_wait_all(uint32_t bar, uint32_t parity, volatile int* dead) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, dead)) != 0;
+__device__ __forceinline__ bool mbar_wait_all(uint32_t bar, uint32_t parity, const Guard& w) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, w)) != 0;
 }
-// The same, bounded, without the give-up flag: used only to let copies in flight land.
+// Once a wait has given up and all threads have stopped: bounded waits that let what is under way land.
 __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
     const long long t0 = clock64();
     while (!mbar_try(bar, parity))
         if (clock64() - t0 > kDrainClocks) return;
+}
+__device__ __forceinline__ void drain_pause() {
+    const long long t0 = clock64();
+    while (clock64() - t0 < kDrainClocks) {}
 }
 
 // Programmatic launches. grid_wait: until the kernels before this one on the stream have ended and
@@ -108,6 +126,9 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
+}
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;

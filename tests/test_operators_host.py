@@ -1,4 +1,5 @@
-"""What the prompt operators refuse on the host, without a GPU: sizes whose 32-bit indices would not hold."""
+"""What the prompt operators refuse on the host, without a GPU: sizes whose 32-bit indices would not hold, a
+limit of no time."""
 
 import pytest
 
@@ -21,3 +22,9 @@ def test_a_k_whose_steps_pass_32_bits(m, k):
     g = kd.kd_gated_args(dtype=0, act=2, m=m, d=k, f=4, x=P, ld_x=LD, wg=P, ld_wg=LD, wu=P, ld_wu=LD)
     assert kd.load_library().kd_gated_ffn(bytes(g), P, 8, None) == -1
     assert b"range" in kd.load_library().kd_op_error()
+
+
+def test_a_limit_of_no_time():
+    lib = kd.load_library()
+    assert lib.kd_op_set_timeout(0) == -1 and lib.kd_op_set_timeout(-5) == -1
+    assert lib.kd_op_set_timeout((1 << 63) - 1) == 0 and lib.kd_op_set_timeout(2_000_000_000) == 0
