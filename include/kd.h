@@ -143,7 +143,8 @@ int kd_reset(kd_ctx *ctx, const int32_t *d_tokens, int32_t n_tokens, int32_t kv_
  * call's kernels run) may go away once the stream has passed the call. With a workspace of
  * kd_prefill_workspace() bytes for n_tokens the prompt goes through in one piece; a smaller one
  * means several, one that does not hold a single token KD_ENOMEM. kv_len + n_tokens > max_seq:
- * KD_ECAPACITY. A token id outside [0, vocab) is reported by kd_sync (KD_ETOKEN).
+ * KD_ECAPACITY. A token id outside [0, vocab) is reported by kd_sync (KD_ETOKEN), and so is a
+ * device-side wait of these operators that exceeds the limit of kd_set_timeout (KD_ETIMEOUT).
  * Operands of the tensor cores (normalised activations, q, attention outputs, hidden units) are
  * rounded to bf16; kd_decode keeps those in fp32, so the cache differs from the one it would
  * have written by such roundings. */
@@ -168,7 +169,8 @@ int kd_generate(kd_ctx *ctx, const int32_t *h_tokens, int32_t n_tokens, int32_t 
                 int32_t n_gen, int32_t *h_tokens_out);
 
 /* Time limit, in nanoseconds (>= 1), of every device-side wait of later launches: a
- * cross-CTA sync, a weight stage, a tagged activation, a KV-row guard. The default is 1 s, or
+ * cross-CTA sync, a weight stage, a tagged activation, a KV-row guard, and in kd_prefill (which
+ * counts in SM clocks, two a nanosecond) a tile of operands or of sums. The default is 1 s, or
  * KD_TIMEOUT_MS milliseconds when that environment variable is set at kd_create. A wait that
  * exceeds its limit sets the device status and every CTA stops (none traps, none hangs:
  * copies already in flight are awaited under a separate fixed bound); kd_sync then returns
@@ -317,9 +319,10 @@ size_t kd_prompt_attention_workspace(const kd_attention_args *args);
 int kd_prompt_attention(const kd_attention_args *args, void *stream);
 
 /* Time limit, in nanoseconds (>= 1; default 2 s), of every device-side wait of the calling thread's
- * later operator calls, counted in SM clocks at two a nanosecond: about the limit, not less. A wait that
- * exceeds it sets the device's status and its kernel ends early (none traps, none hangs: copies and
- * products under way are awaited under a separate fixed bound); its outputs are not valid. */
+ * later operator calls, counted in SM clocks at two a nanosecond: about the limit, not less. A wait
+ * that exceeds it sets the device's status and its kernel ends early (none traps, none hangs: copies
+ * and products under way are awaited under a separate fixed bound); its outputs are not valid. (Those
+ * of kd_prefill are under kd_set_timeout and reported by kd_sync.) */
 int kd_op_set_timeout(int64_t ns);
 
 /* Wait for `stream` and report whether a device-side wait of an operator has run out of its limit on the

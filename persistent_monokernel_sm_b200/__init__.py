@@ -373,7 +373,8 @@ class Decoder:
 
     def prefill(self, tokens, kv_len: int = 0, max_piece: int = 4096):
         """reset() for a prompt: all but its last token run through the layers now, on the tensor
-        cores, at most max_piece tokens at once; the last one is pending for decode()."""
+        cores, at most max_piece tokens at once; the last one is pending for decode(). A bad token or
+        a wait that exceeds the handle's limit is reported by sync()."""
         torch = self.torch
         if max_piece < 1:
             raise KdError(-1, "prefill: max_piece must be at least 1")

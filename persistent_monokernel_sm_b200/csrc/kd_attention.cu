@@ -58,7 +58,7 @@ struct AttnArgs {
     float scale_log2;
     void* out;
     int64_t out_token, out_head;
-    long long limit;  // of a wait, in SM clocks
+    OpWaits waits;
 };
 
 template <int HD> struct Shape {
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kThr, 1)
     const uint32_t ring = qs + 2 * kBlock;
     const uint32_t full = smem_u32(s_full), empty = smem_u32(s_empty), qbar = smem_u32(&s_q);
     const uint32_t sbar = smem_u32(s_s), pbar = smem_u32(s_p), obar = smem_u32(s_o), drain = smem_u32(&s_drain);
-    const Guard dead{&s_dead, a.limit};
+    const Guard dead{&s_dead, a.waits};
     // (m, l) of the two streams' rows for the join: where a second query tile would be
     float* stat = reinterpret_cast<float*>(smem_raw + (qs + kBlock - smem_u32(smem_raw)));
     auto part_at = [&](int s, int row) {  // a row's partial output, where the blocks were
@@ -615,10 +615,6 @@ int attention_status(cudaStream_t s, unsigned int* st) {
     return e == cudaSuccess ? KD_OK : op_fail(KD_ECUDA, "kd_op_sync: %s", cudaGetErrorString(e));
 }
 
-}  // namespace kd
-
-using namespace kd;
-
 static int check_attention(const kd_attention_args& q) {
     if (q.dtype != KD_BF16 && q.dtype != KD_F16)
         return op_fail(KD_EINVAL, "kd_prompt_attention: dtype must be KD_BF16 or KD_F16");
@@ -632,12 +628,7 @@ static int check_attention(const kd_attention_args& q) {
     return KD_OK;
 }
 
-extern "C" size_t kd_prompt_attention_workspace(const kd_attention_args* p) {
-    if (!p || check_attention(*p) || p->n == 0) return 0;
-    return (size_t)cut_of(p->n, p->kv_len, p->n_heads / p->n_kv_heads, p->n_kv_heads, p->head_dim).bytes;
-}
-
-extern "C" int kd_prompt_attention(const kd_attention_args* p, void* stream) {
+int attention_op(const kd_attention_args* p, const OpWaits& waits, cudaStream_t s) {
     if (!p) return op_fail(KD_EINVAL, "kd_prompt_attention: NULL arguments");
     kd_attention_args q = *p;
     int rc = check_attention(q);
@@ -673,7 +664,7 @@ extern "C" int kd_prompt_attention(const kd_attention_args* p, void* stream) {
                        (size_t)c.bytes);
     a.shared = c.shared, a.splits = c.splits;
     a.parts = (float*)(((uintptr_t)q.workspace + 255) & ~(uintptr_t)255);
-    a.limit = op_limit();
+    a.waits = waits;
     const int64_t grid = c.grid;
     const bool bf = q.dtype == KD_BF16;
     CUtensorMap mq, mk, mv;
@@ -684,8 +675,20 @@ extern "C" int kd_prompt_attention(const kd_attention_args* p, void* stream) {
     if ((rc = make_map_3d(&mv, q.dtype, q.v, q.head_dim, T, a.hkv, q.v_pos, q.v_head, 64, kKeys, 1))) return rc;
     a.idesc_s = make_idesc(128, kKeys, bf, false, false);
     a.idesc_o = make_idesc(128, q.head_dim, bf, false, true);
-    cudaStream_t s = (cudaStream_t)stream;
     if (q.head_dim == 128)
         return bf ? launch<128, __nv_bfloat16>(mq, mk, mv, a, (int)grid, s) : launch<128, __half>(mq, mk, mv, a, (int)grid, s);
     return bf ? launch<64, __nv_bfloat16>(mq, mk, mv, a, (int)grid, s) : launch<64, __half>(mq, mk, mv, a, (int)grid, s);
+}
+
+}  // namespace kd
+
+using namespace kd;
+
+extern "C" size_t kd_prompt_attention_workspace(const kd_attention_args* p) {
+    if (!p || check_attention(*p) || p->n == 0) return 0;
+    return (size_t)cut_of(p->n, p->kv_len, p->n_heads / p->n_kv_heads, p->n_kv_heads, p->head_dim).bytes;
+}
+
+extern "C" int kd_prompt_attention(const kd_attention_args* p, void* stream) {
+    return attention_op(p, own_waits(), (cudaStream_t)stream);
 }

@@ -65,9 +65,8 @@ int op_sm_count(int* sms) {
     return KD_OK;
 }
 
-// Per calling thread. SM clocks run at less than two a nanosecond.
 static thread_local long long t_limit_ns = 2000000000ll;
-long long op_limit() { return 2 * (t_limit_ns < (1ll << 61) ? t_limit_ns : 1ll << 61); }
+OpWaits own_waits() { return {op_clocks(t_limit_ns), nullptr}; }
 
 typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -185,7 +184,7 @@ struct GemmArgs {
     // waited for: it starts beside it, and waits for its end before its own.
     int beside;
     int t_half;  // token tiles of the first of two products with the same A; 0: one product
-    long long limit;  // of a wait, in SM clocks
+    OpWaits waits;
 };
 
 // ------------------------------------------------------------------ activations
@@ -430,7 +429,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    const Guard dead{&s_dead, g.limit};
+    const Guard dead{&s_dead, g.waits};
     // What came before on the stream may still run until here; the next launch may start its own
     // set-up as this one's CTAs end.
     if (!g.beside) grid_wait();
@@ -1053,7 +1052,6 @@ int run_typed(GemmArgs g, int dtype, const Operand* a, const Operand* b, int pai
     if (EPI == EPI_GATED_BWD) g.ld_out2 = g.ld_out;
     int64_t ld[2] = {g.ld_out, g.ld_out2};
     const void* out[2] = {g.out, g.out2};
-    g.limit = op_limit();
     g.tma_out = 1;
     for (int i = 0; i < 2; ++i) {
         if (g.M == 1) ld[i] = (g.N + 7) & ~(int64_t)7;  // one row: its distance to the next is not used
@@ -1132,6 +1130,60 @@ int gemm_status(cudaStream_t s, unsigned int* st) {
     return e == cudaSuccess ? KD_OK : op_fail(KD_ECUDA, "kd_op_sync: %s", cudaGetErrorString(e));
 }
 
+int linear_op(const kd_linear_args* p, const OpWaits& waits, cudaStream_t s) {
+    if (!p) return op_fail(KD_EINVAL, "kd_linear: NULL arguments");
+    kd_linear_args q = *p;
+    int rc = check_sizes("kd_linear", q.dtype, q.act, q.m, q.n, q.k);
+    if (rc) return rc;
+    if (q.out_dtype != q.dtype && q.out_dtype != KD_F32)
+        return op_fail(KD_EINVAL, "kd_linear: out_dtype must be the input type or KD_F32");
+    if (q.w_transposed != 0 && q.w_transposed != 1) return op_fail(KD_EINVAL, "kd_linear: w_transposed must be 0 or 1");
+    if (q.m == 0 || q.n == 0) return KD_OK;
+    const int oe = q.out_dtype == KD_F32 ? 4 : 2;
+    if ((rc = check_operand("kd_linear: x", q.x, q.m, q.k, &q.ld_x))) return rc;
+    if ((rc = check_operand("kd_linear: w", q.w, q.w_transposed ? q.k : q.n, q.w_transposed ? q.n : q.k, &q.ld_w))) return rc;
+    if (q.bias && (uintptr_t)q.bias % 2) return op_fail(KD_EINVAL, "kd_linear: bias: misaligned pointer");
+    if (q.residual && (rc = check_rows("kd_linear: residual", q.residual, oe, q.m, q.n, q.ld_residual))) return rc;
+    if ((rc = check_rows("kd_linear: out", q.out, oe, q.m, q.n, q.ld_out))) return rc;
+    if (few_tokens(q.m, q.n, q.k, 1) && !q.w_transposed) {
+        const RowArgs r{q.x, q.w, nullptr, q.bias, q.residual, q.out, q.ld_x, q.ld_w, 0, q.ld_residual, q.ld_out, q.n, (int)q.k, (int)q.m, q.act};
+        if (q.dtype == KD_BF16)
+            return q.out_dtype == KD_F32 ? run_rows<false, __nv_bfloat16, float>(r, s) : run_rows<false, __nv_bfloat16, __nv_bfloat16>(r, s);
+        return q.out_dtype == KD_F32 ? run_rows<false, __half, float>(r, s) : run_rows<false, __half, __half>(r, s);
+    }
+    GemmArgs g{};
+    g.N = q.n, g.M = q.m, g.act = q.act, g.waits = waits;
+    g.bias = q.bias, g.res = q.residual, g.ld_res = q.ld_residual, g.out = q.out, g.ld_out = q.ld_out;
+    const Operand a{q.w, q.ld_w, q.w_transposed != 0}, b{q.x, q.ld_x, false};
+    return run<EPI_LINEAR>(g, q.dtype, q.out_dtype, &a, &b, 1, q.k, s);
+}
+
+static int check_gated(const char* who, kd_gated_args* q) {
+    int rc = check_sizes(who, q->dtype, q->act, q->m, q->f, q->d);
+    if (rc) return rc;
+    if (q->m == 0 || q->f == 0) return KD_OK;
+    if ((rc = check_operand("gated block: x", q->x, q->m, q->d, &q->ld_x))) return rc;
+    if ((rc = check_operand("gated block: wg", q->wg, q->f, q->d, &q->ld_wg))) return rc;
+    return check_operand("gated block: wu", q->wu, q->f, q->d, &q->ld_wu);
+}
+
+int gated_op(const kd_gated_args* p, void* h, int64_t ld_h, const OpWaits& waits, cudaStream_t s) {
+    if (!p) return op_fail(KD_EINVAL, "kd_gated_ffn: NULL arguments");
+    kd_gated_args q = *p;
+    int rc = check_gated("kd_gated_ffn", &q);
+    if (rc || q.m == 0 || q.f == 0) return rc;
+    if ((rc = check_rows("kd_gated_ffn: h", h, 2, q.m, q.f, ld_h))) return rc;
+    if (few_tokens(q.m, q.f, q.d, 2)) {
+        const RowArgs r{q.x, q.wg, q.wu, nullptr, nullptr, h, q.ld_x, q.ld_wg, q.ld_wu, 0, ld_h, q.f, (int)q.d, (int)q.m, q.act};
+        return q.dtype == KD_BF16 ? run_rows<true, __nv_bfloat16, __nv_bfloat16>(r, s)
+                                  : run_rows<true, __half, __half>(r, s);
+    }
+    GemmArgs g{};
+    g.N = q.f, g.M = q.m, g.act = q.act, g.out = h, g.ld_out = ld_h, g.waits = waits;
+    const Operand a[2] = {{q.wg, q.ld_wg, false}, {q.wu, q.ld_wu, false}}, b{q.x, q.ld_x, false};
+    return run<EPI_GATED>(g, q.dtype, q.dtype, a, &b, 2, q.d, s);
+}
+
 }  // namespace kd
 
 using namespace kd;
@@ -1155,59 +1207,10 @@ int kd_op_sync(void* stream) {
     return KD_OK;
 }
 
-int kd_linear(const kd_linear_args* p, void* stream) {
-    if (!p) return op_fail(KD_EINVAL, "kd_linear: NULL arguments");
-    kd_linear_args q = *p;
-    int rc = check_sizes("kd_linear", q.dtype, q.act, q.m, q.n, q.k);
-    if (rc) return rc;
-    if (q.out_dtype != q.dtype && q.out_dtype != KD_F32)
-        return op_fail(KD_EINVAL, "kd_linear: out_dtype must be the input type or KD_F32");
-    if (q.w_transposed != 0 && q.w_transposed != 1) return op_fail(KD_EINVAL, "kd_linear: w_transposed must be 0 or 1");
-    if (q.m == 0 || q.n == 0) return KD_OK;
-    const int oe = q.out_dtype == KD_F32 ? 4 : 2;
-    if ((rc = check_operand("kd_linear: x", q.x, q.m, q.k, &q.ld_x))) return rc;
-    if ((rc = check_operand("kd_linear: w", q.w, q.w_transposed ? q.k : q.n, q.w_transposed ? q.n : q.k, &q.ld_w))) return rc;
-    if (q.bias && (uintptr_t)q.bias % 2) return op_fail(KD_EINVAL, "kd_linear: bias: misaligned pointer");
-    if (q.residual && (rc = check_rows("kd_linear: residual", q.residual, oe, q.m, q.n, q.ld_residual))) return rc;
-    if ((rc = check_rows("kd_linear: out", q.out, oe, q.m, q.n, q.ld_out))) return rc;
-    if (few_tokens(q.m, q.n, q.k, 1) && !q.w_transposed) {
-        const RowArgs r{q.x, q.w, nullptr, q.bias, q.residual, q.out, q.ld_x, q.ld_w, 0, q.ld_residual, q.ld_out, q.n, (int)q.k, (int)q.m, q.act};
-        cudaStream_t s = (cudaStream_t)stream;
-        if (q.dtype == KD_BF16)
-            return q.out_dtype == KD_F32 ? run_rows<false, __nv_bfloat16, float>(r, s) : run_rows<false, __nv_bfloat16, __nv_bfloat16>(r, s);
-        return q.out_dtype == KD_F32 ? run_rows<false, __half, float>(r, s) : run_rows<false, __half, __half>(r, s);
-    }
-    GemmArgs g{};
-    g.N = q.n, g.M = q.m, g.act = q.act;
-    g.bias = q.bias, g.res = q.residual, g.ld_res = q.ld_residual, g.out = q.out, g.ld_out = q.ld_out;
-    const Operand a{q.w, q.ld_w, q.w_transposed != 0}, b{q.x, q.ld_x, false};
-    return run<EPI_LINEAR>(g, q.dtype, q.out_dtype, &a, &b, 1, q.k, (cudaStream_t)stream);
-}
-
-static int check_gated(const char* who, kd_gated_args* q) {
-    int rc = check_sizes(who, q->dtype, q->act, q->m, q->f, q->d);
-    if (rc) return rc;
-    if (q->m == 0 || q->f == 0) return KD_OK;
-    if ((rc = check_operand("gated block: x", q->x, q->m, q->d, &q->ld_x))) return rc;
-    if ((rc = check_operand("gated block: wg", q->wg, q->f, q->d, &q->ld_wg))) return rc;
-    return check_operand("gated block: wu", q->wu, q->f, q->d, &q->ld_wu);
-}
+int kd_linear(const kd_linear_args* p, void* stream) { return linear_op(p, own_waits(), (cudaStream_t)stream); }
 
 int kd_gated_ffn(const kd_gated_args* p, void* h, int64_t ld_h, void* stream) {
-    if (!p) return op_fail(KD_EINVAL, "kd_gated_ffn: NULL arguments");
-    kd_gated_args q = *p;
-    int rc = check_gated("kd_gated_ffn", &q);
-    if (rc || q.m == 0 || q.f == 0) return rc;
-    if ((rc = check_rows("kd_gated_ffn: h", h, 2, q.m, q.f, ld_h))) return rc;
-    if (few_tokens(q.m, q.f, q.d, 2)) {
-        const RowArgs r{q.x, q.wg, q.wu, nullptr, nullptr, h, q.ld_x, q.ld_wg, q.ld_wu, 0, ld_h, q.f, (int)q.d, (int)q.m, q.act};
-        return q.dtype == KD_BF16 ? run_rows<true, __nv_bfloat16, __nv_bfloat16>(r, (cudaStream_t)stream)
-                                  : run_rows<true, __half, __half>(r, (cudaStream_t)stream);
-    }
-    GemmArgs g{};
-    g.N = q.f, g.M = q.m, g.act = q.act, g.out = h, g.ld_out = ld_h;
-    const Operand a[2] = {{q.wg, q.ld_wg, false}, {q.wu, q.ld_wu, false}}, b{q.x, q.ld_x, false};
-    return run<EPI_GATED>(g, q.dtype, q.dtype, a, &b, 2, q.d, (cudaStream_t)stream);
+    return gated_op(p, h, ld_h, own_waits(), (cudaStream_t)stream);
 }
 
 static int64_t gated_ld(int64_t f) { return (f + 63) & ~(int64_t)63; }
@@ -1242,12 +1245,14 @@ int kd_gated_ffn_backward(const kd_gated_args* p, const void* dh, int64_t ld_dh,
     // of a sum is of the size of the rounding of its result.
     {
         GemmArgs g{};
+        g.waits = own_waits();
         g.N = q.f, g.M = q.m, g.act = q.act, g.res = dh, g.ld_res = ld_dh, g.out = dg, g.out2 = du, g.ld_out = ld;
         const Operand a[2] = {{q.wg, q.ld_wg, false}, {q.wu, q.ld_wu, false}}, b{q.x, q.ld_x, false};
         if ((rc = run<EPI_GATED_BWD>(g, q.dtype, q.dtype, a, &b, 2, q.d, s))) return rc;
     }
     if (dx) {  // dx[t][c] = sum_f dg[t][f] wg[f][c] + du[t][f] wu[f][c]: one sum over both pairs
         GemmArgs g{};
+        g.waits = own_waits();
         g.N = q.d, g.M = q.m, g.out = dx, g.ld_out = ld_dx;
         const Operand a[2] = {{q.wg, q.ld_wg, true}, {q.wu, q.ld_wu, true}}, b[2] = {{dg, ld, false}, {du, ld, false}};
         if ((rc = run<EPI_LINEAR>(g, q.dtype, q.dtype, a, b, 2, q.f, s))) return rc;
@@ -1256,6 +1261,7 @@ int kd_gated_ffn_backward(const kd_gated_args* p, const void* dh, int64_t ld_dh,
     const Operand a{q.x, q.ld_x, true}, b[2] = {{dwg ? dg : du, ld, true}, {du, ld, true}};
     if (dwg || dwu) {
         GemmArgs g{};
+        g.waits = own_waits();
         g.N = q.d, g.M = q.f;
         g.out = dwg ? dwg : dwu, g.ld_out = dwg ? ld_dwg : ld_dwu;
         g.out2 = dwu, g.ld_out2 = ld_dwu;

@@ -49,6 +49,7 @@ constexpr int kSumCopies = 2;
 
 constexpr int kStatusTimeout = 1;  // a device-side wait exceeded its limit
 constexpr int kStatusToken = 2;    // a token id outside [0, vocab) reached the kernel
+constexpr int kWhereOperator = 7;  // beside kd_kernel.cu's kinds: a wait of one of kd_prefill's operators
 
 struct Dims {
     int L, d, Hq, Hkv, hd, F, V, S;  // S = max_seq

@@ -185,6 +185,7 @@ int kd_prefill(kd_ctx* c, const int32_t* d_tokens, int32_t n_tokens, int32_t kv_
     float* qkv = (float*)(base + sp.qkv);
     const int64_t ldh = hidden_ld(d.F);
     unsigned long long* ctl = (unsigned long long*)(v.arena + y.ctl);
+    const OpWaits waits{op_clocks(v.timeout_ns), ctl};
     auto op = [&](int code) {
         if (code == KD_OK) kd_internal_count_launch(c);
         else kd_internal_fail(c, code, kd_op_error());
@@ -212,7 +213,7 @@ int kd_prefill(kd_ctx* c, const int32_t* d_tokens, int32_t n_tokens, int32_t kv_
             a.dtype = KD_BF16, a.out_dtype = KD_F32;
             a.m = m, a.n = d.qkv_rows, a.k = d.d;
             a.x = xn, a.ld_x = d.d, a.w = w + y.l_wqkv, a.ld_w = d.d, a.out = qkv, a.ld_out = d.qkv_rows;
-            if ((rc = op(kd_linear(&a, s)))) return rc;
+            if ((rc = op(linear_op(&a, waits, s)))) return rc;
             rope_append<<<(unsigned)m, 256, 0, s>>>(qkv, (const float2*)(v.arena + y.rope), q, kc, vc, d, pos0);
             if ((rc = own())) return rc;
             if (l == d.L - 1) break;  // nothing later reads what the last layer does with these tokens
@@ -224,14 +225,14 @@ int kd_prefill(kd_ctx* c, const int32_t* d_tokens, int32_t n_tokens, int32_t kv_
             t.out = att, t.out_token = d.qd, t.out_head = d.hd;
             t.scale = 1.f / sqrtf((float)d.hd);
             t.workspace = base + sp.part, t.workspace_bytes = sp.total - sp.part;
-            if ((rc = op(kd_prompt_attention(&t, s)))) return rc;
+            if ((rc = op(attention_op(&t, waits, s)))) return rc;
             if (kd_prompt_attention_workspace(&t) > 0) kd_internal_count_launch(c);  // and its join
             a = kd_linear_args{};  // x += att wo^T
             a.dtype = KD_BF16, a.out_dtype = KD_F32, a.w_transposed = 1;
             a.m = m, a.n = d.d, a.k = d.qd;
             a.x = att, a.ld_x = d.qd, a.w = w + y.l_wot, a.ld_w = d.d;
             a.residual = x, a.ld_residual = d.d, a.out = x, a.ld_out = d.d;
-            if ((rc = op(kd_linear(&a, s)))) return rc;
+            if ((rc = op(linear_op(&a, waits, s)))) return rc;
             norm_rows<<<(unsigned)m, kNormThreads, 0, s>>>(x, xn, (const __nv_bfloat16*)(w + y.l_ffn_norm), d.d, d.eps,
                                                           nullptr, nullptr, 0, nullptr);
             if ((rc = own())) return rc;
@@ -240,10 +241,10 @@ int kd_prefill(kd_ctx* c, const int32_t* d_tokens, int32_t n_tokens, int32_t kv_
             f.m = m, f.d = d.d, f.f = d.F;
             f.x = xn, f.ld_x = d.d;
             f.wg = w + y.l_wgu, f.wu = w + y.l_wgu + (size_t)d.d * 2, f.ld_wg = f.ld_wu = 2 * (int64_t)d.d;
-            if ((rc = op(kd_gated_ffn(&f, h, ldh, s)))) return rc;
+            if ((rc = op(gated_op(&f, h, ldh, waits, s)))) return rc;
             a.k = d.F;  // x += h wd^T
             a.x = h, a.ld_x = ldh, a.w = w + y.l_wdt;
-            if ((rc = op(kd_linear(&a, s)))) return rc;
+            if ((rc = op(linear_op(&a, waits, s)))) return rc;
         }
     }
     return KD_OK;

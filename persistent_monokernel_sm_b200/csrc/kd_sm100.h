@@ -9,17 +9,21 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "kd_layout.h"
+#include "kd_ops.h"
+
 namespace kd {
 
-// Set by a wait that ran out of its limit (one word per source file that includes this);
-// kd_op_sync reads and clears them.
+// Set by a wait that ran out of its limit, unless a handle's control words are (one word per source
+// file that includes this); kd_op_sync reads and clears them.
 static __device__ unsigned int g_op_status;
 
-// What a CTA's waits go by: its give-up flag and their limit in SM clocks. The waits read the SM's
-// own clock: a read of the global timer costs about as much as the wait it would guard.
+// What a CTA's waits go by: its give-up flag, their limit in SM clocks, and the control words of the
+// handle that reports one which runs out (NULL: g_op_status does). The waits read the SM's own
+// clock: a read of the global timer costs about as much as the wait it would guard.
 struct Guard {
     volatile int* dead;
-    long long limit;
+    OpWaits waits;
 };
 constexpr long long kSuspendClocks = 1 << 20;    // more than try_wait suspends a thread for
 constexpr long long kDrainClocks = 200000000ll;  // of the wait for copies in flight: about 0.1 s
@@ -74,7 +78,9 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
 }
 __device__ __forceinline__ void raise_timeout(const Guard& w) {
     *w.dead = 1;
-    atomicExch(&g_op_status, 1u);
+    if (!w.waits.ctl) atomicExch(&g_op_status, 1u);
+    else if (atomicCAS(w.waits.ctl + kCtlStatus, 0ull, (unsigned long long)kStatusTimeout) == 0ull)
+        atomicExch(w.waits.ctl + kCtlWhere, ((unsigned long long)kWhereOperator << 24) | (unsigned long long)((blockIdx.x & 0xffff) << 8));
 }
 // Waits until the phase of `parity` has completed. Gives up when the limit has passed or
 // another wait of this CTA has given up (*dead), and then returns false: the caller unwinds.
@@ -84,7 +90,7 @@ __device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, co
         for (int i = 0; i < 32; ++i)
             if (mbar_try(bar, parity)) return true;
         if (*w.dead) return false;
-        if (clock64() - t0 > w.limit) {
+        if (clock64() - t0 > w.waits.limit) {
             raise_timeout(w);
             return false;
         }
@@ -97,7 +103,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const G
 // A first look at a kernel's first barrier: within a limit that is shorter than a thread may be suspended for,
 // it gives up at once unless the phase has completed.
 __device__ __forceinline__ bool mbar_first(uint32_t bar, uint32_t parity, const Guard& w) {
-    if (__builtin_expect(w.limit >= kSuspendClocks, 1) || mbar_test(bar, parity)) return true;
+    if (__builtin_expect(w.waits.limit >= kSuspendClocks, 1) || mbar_test(bar, parity)) return true;
     raise_timeout(w);
     return false;
 }
