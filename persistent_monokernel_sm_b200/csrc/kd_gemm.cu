@@ -140,11 +140,14 @@ namespace {
 // epilogue takes registers from the third: 256 x 216 + 128 x 72 = 384 x 168, the launch's total.
 constexpr int kGemmThreads = 384;
 constexpr int kEpiRegs = 216, kAuxRegs = 72;
-// An accumulator of the tensor cores is truncated at every step of 16 products (measured:
-// 1.7e-8 relative per step, all towards zero, 4.3e-6 at k = 4,096). Where the result is kept in
-// fp32, sums of more than 512 products are therefore taken as several, added in registers with
-// rounding to nearest. A 16-bit result does not show it (2^-9 and 2^-12).
-constexpr int kChunk = 8;  // 64-deep k-blocks
+// An accumulator of the tensor cores is truncated towards zero at every step of 16 products. Measured,
+// relative: 9.8e-8 a step where all terms have one sign (1e-3 over 2^17 products), 1.7e-8 where signs are
+// mixed (4.3e-6 at k = 4,096). Where the result is kept in fp32, sums of more than 512 products are
+// therefore taken as several, added in registers with rounding to nearest. A result of 16 bits does not
+// show it until its sum is long: the same is done for it from 2^15 products of a CTA in fp16 and 2^18 in
+// bf16 on, where the truncation could reach 0.41 of the type's half step (2^-11, 2^-8).
+constexpr int kChunk = 8;                        // 64-deep k-blocks
+constexpr int kLongF16 = 512, kLongBF16 = 4096;  // k-blocks
 constexpr int kBK = 64;            // k-block: 128 bytes of a row
 constexpr int kABytes = 128 * kBK * 2;
 constexpr int kMaxRing = 12;
@@ -386,7 +389,8 @@ __device__ __noinline__ void unwind_loads(uint32_t full, int stages, int loads) 
     }
 }
 
-template <int CG, int EPI, int LAY, typename T, typename O>
+// LONG: a 16-bit result of a sum that is taken as several.
+template <int CG, int EPI, int LAY, typename T, typename O, bool LONG>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap a0, const __grid_constant__ CUtensorMap a1,
                 const __grid_constant__ CUtensorMap b0, const __grid_constant__ CUtensorMap b1,
@@ -399,7 +403,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     __shared__ int s_loads;  // the producer's
 
     constexpr bool kAMn = LAY != LAY_KK, kBMn = LAY == LAY_MM;
-    constexpr bool kSums = EPI == EPI_LINEAR && sizeof(O) == 4;  // add sums of kStep k-blocks
+    constexpr bool kSums = EPI == EPI_LINEAR && (sizeof(O) == 4 || LONG);  // add sums of kStep k-blocks
     constexpr int kStep = kSums ? kChunk : 1 << 28;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t ring = (smem_u32(smem_raw) + 1023) & ~1023u;
@@ -942,13 +946,13 @@ Plan make_plan(int64_t n_tiles, int64_t M, int kb, int sms, const int* room, boo
     return best;
 }
 
-template <int CG, int EPI, int LAY, typename T, typename O>
+template <int CG, int EPI, int LAY, typename T, typename O, bool LONG = false>
 int launch(const CUtensorMap* m, const GemmArgs& g, int grid, cudaStream_t stream) {
     int dev = 0;
     cudaGetDevice(&dev);
     static std::atomic<bool> ready[64];
     if (dev >= 64 || !ready[dev].load()) {
-        cudaError_t e = cudaFuncSetAttribute(gemm_kernel<CG, EPI, LAY, T, O>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(gemm_kernel<CG, EPI, LAY, T, O, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              kSmemBytes);
         if (e != cudaSuccess) return op_fail(KD_ECUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
         if (dev < 64) ready[dev].store(true);
@@ -966,7 +970,7 @@ int launch(const CUtensorMap* m, const GemmArgs& g, int grid, cudaStream_t strea
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = CG == 2 || g.splits > 1 ? 2 : 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_kernel<CG, EPI, LAY, T, O>, m[0], m[1], m[2], m[3], m[4], m[5], g);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_kernel<CG, EPI, LAY, T, O, LONG>, m[0], m[1], m[2], m[3], m[4], m[5], g);
     if (e != cudaSuccess) return op_fail(KD_ECUDA, "launch failed: %s", cudaGetErrorString(e));
     return KD_OK;
 }
@@ -979,7 +983,7 @@ int cluster_room(int sms, int room[9]) {
     for (int i = 0, s = 2; s <= 8; ++i, s *= 2) {
         int n = dev < 64 ? cached[dev][i].load() : 0;
         if (n == 0) {
-            const auto kernel = gemm_kernel<1, EPI_LINEAR, LAY_KK, __nv_bfloat16, __nv_bfloat16>;
+            const auto kernel = gemm_kernel<1, EPI_LINEAR, LAY_KK, __nv_bfloat16, __nv_bfloat16, false>;
             e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
             cudaLaunchConfig_t cfg{};
             cfg.gridDim = dim3(sms / s * s);
@@ -1027,7 +1031,8 @@ int run_typed(GemmArgs g, int dtype, const Operand* a, const Operand* b, int pai
     if (n_tiles * t_tiles > 0x3fffffff) return op_fail(KD_EINVAL, "too many output tiles");
     // Pairs of CTAs where they take no more rounds than single ones.
     const int64_t pair_tiles = (n_tiles + 1) / 2 * t_tiles;
-    const bool pair = p.splits == 1 && p.bn >= kPairMin && p.bn % (b[0].mn ? 128 : 64) == 0 && n_tiles > 1 && room[2] >= sms / 2 &&
+    const bool pieces = EPI == EPI_LINEAR && sizeof(O) == 2 && g.kb / p.splits > (dtype == KD_BF16 ? kLongBF16 : kLongF16);
+    const bool pair = !pieces && p.splits == 1 && p.bn >= kPairMin && p.bn % (b[0].mn ? 128 : 64) == 0 && n_tiles > 1 && room[2] >= sms / 2 &&
                       (pair_tiles + sms / 2 - 1) / (sms / 2) <= (n_tiles * t_tiles + sms - 1) / sms;
     const int cg = pair ? 2 : 1;
     const int grid = pair ? 2 * (int)(pair_tiles < sms / 2 ? pair_tiles : sms / 2) : p.grid;
@@ -1064,6 +1069,11 @@ int run_typed(GemmArgs g, int dtype, const Operand* a, const Operand* b, int pai
         if (two && (rc = make_map_out(&m[5], out_type, out[1], g.N, g.M, ld[1], gated ? 16 : 32, rows))) return rc;
     }
     if constexpr (EPI == EPI_LINEAR) {
+        if constexpr (sizeof(O) == 2)
+            if (pieces)
+                return b[0].mn   ? launch<1, EPI, LAY_MM, T, O, true>(m, g, grid, stream)
+                       : a[0].mn ? launch<1, EPI, LAY_MK, T, O, true>(m, g, grid, stream)
+                                 : launch<1, EPI, LAY_KK, T, O, true>(m, g, grid, stream);
         if constexpr (sizeof(O) == 2)  // the weights' gradients
             if (b[0].mn) return pair ? launch<2, EPI, LAY_MM, T, O>(m, g, grid, stream) : launch<1, EPI, LAY_MM, T, O>(m, g, grid, stream);
         if (a[0].mn) return pair ? launch<2, EPI, LAY_MK, T, O>(m, g, grid, stream) : launch<1, EPI, LAY_MK, T, O>(m, g, grid, stream);

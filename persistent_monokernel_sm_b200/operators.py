@@ -5,7 +5,9 @@ enqueue kd_linear, kd_gated_ffn, ... (include/kd.h) on the current stream of the
 all of that is in csrc/kd_torch.cpp. Tensors are bfloat16 or float16 and their last dimension is
 contiguous; rows of a product's inputs start on 16 bytes (a row stride that is a multiple of 8
 elements). The functions record no autograd graph: gated_ffn_backward returns the gradients. What
-they refuse raises KdError.
+they refuse raises KdError. A device-side wait that exceeds its limit (kd_op_set_timeout; none comes
+near the default of 2 s) ends its kernel early with outputs that are not valid: kd_op_sync waits for
+a stream and raises KdError (KD_ETIMEOUT) then.
 """
 
 from __future__ import annotations
