@@ -1,7 +1,8 @@
 // kd_torch.cpp -- the prompt operators on torch tensors, as the Python module _kd_torch: checks,
 // allocation of the outputs and workspaces with torch's allocator, and the call into libkd on the
 // current stream of the tensors' device. The same in Python takes 6 to 9 us a call, more than a
-// token's products take on the GPU; here it takes 1 to 2. No autograd graph is recorded.
+// token's products take on the GPU; here it takes 1 to 2. No autograd graph is recorded: where gradients are
+// enabled, a tensor that requires them is refused.
 //
 // The functions take their arguments by position (operators.py, which documents them, gives names
 // and defaults) and raise the package's KdError.
@@ -10,6 +11,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/core/LegacyTypeDispatch.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -64,8 +66,19 @@ struct Kind {  // of a call: its input type and device
     int code, dev;
 };
 
+void no_graph_lost(const char* name, const at::Tensor& t) {
+    if (t.requires_grad() && c10::GradMode::is_enabled())
+        refuse("%s requires grad, and no graph is recorded: call under torch.no_grad() or in an autograd.Function", name);
+}
+
+// torch's count of in-place changes, by which a backward pass notices that a value it needs is gone.
+void changed(const at::Tensor& t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // The first input of `dim` dimensions, which sets type and device.
 Kind kind_of(const char* name, const at::Tensor& t, int64_t dim) {
+    no_graph_lost(name, t);
     if (t.dim() != dim || !t.is_cuda()) refuse("%s must be a %d-D CUDA tensor: got %s on %s", name, (int)dim, shape_of(t).c_str(), t.device().str().c_str());
     const auto type = t.scalar_type();
     if (type != at::kBFloat16 && type != at::kHalf) refuse("%s must be bfloat16 or float16: got %s", name, c10::toString(type));
@@ -73,6 +86,7 @@ Kind kind_of(const char* name, const at::Tensor& t, int64_t dim) {
 }
 
 void same(const char* name, const at::Tensor& t, at::ScalarType type, int dev) {
+    no_graph_lost(name, t);
     if (!t.is_cuda() || t.scalar_type() != type || t.get_device() != dev)
         refuse("%s must be a %s tensor on cuda:%d: got %s on %s", name, c10::toString(type), dev, c10::toString(t.scalar_type()), t.device().str().c_str());
 }
@@ -128,7 +142,8 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         const Kind k = kind_of("x", x, 2);
         if (w.dim() != 2) refuse("w must be a 2-D tensor");
         kd_linear_args q{};
-        q.w_transposed = PyObject_IsTrue(a[7]) == 1;
+        q.w_transposed = PyObject_IsTrue(a[7]);
+        if (q.w_transposed < 0) throw Refused();
         q.m = x.size(0), q.k = x.size(1), q.n = w.size(q.w_transposed ? 1 : 0);
         q.dtype = k.code;
         q.act = act_id(a[3]);
@@ -168,6 +183,7 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         }
         check(kd_linear(&q, stream_of(k.dev)));
         if (a[5] == Py_None) return THPVariable_Wrap(std::move(fresh));
+        changed(tensor("out", a[5]));
         Py_INCREF(a[5]);
         return a[5];
     });
@@ -201,6 +217,7 @@ PyObject* gated_ffn(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         const at::Tensor& o = tensor("out", a[4]);
         const int64_t ld = matrix("out", o, q.m, q.f, k.type, k.dev);
         check(kd_gated_ffn(&q, o.data_ptr(), ld, stream_of(k.dev)));
+        changed(o);
         Py_INCREF(a[4]);
         return a[4];
     });
@@ -246,6 +263,7 @@ PyObject* prompt_attention(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         p.kv_len = PyLong_AsLongLong(a[3]);
         if (p.kv_len == -1 && PyErr_Occurred()) throw Refused();
         if (p.kv_len < 0) refuse("kv_len must not be negative");
+        if (p.kv_len > INT32_MAX) refuse("kv_len is out of range");
         const int64_t hd = q.size(2);
         for (int i = 0; i < 2; ++i) {
             const at::Tensor& t = i ? v : k;
@@ -283,6 +301,7 @@ PyObject* prompt_attention(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         }
         check(kd_prompt_attention(&p, stream_of(kind.dev)));
         if (a[5] == Py_None) return THPVariable_Wrap(std::move(out));
+        changed(out);
         Py_INCREF(a[5]);
         return a[5];
     });

@@ -4,10 +4,13 @@ They check shapes, types and devices, allocate outputs and workspaces with torch
 enqueue kd_linear, kd_gated_ffn, ... (include/kd.h) on the current stream of the tensors' device;
 all of that is in csrc/kd_torch.cpp. Tensors are bfloat16 or float16 and their last dimension is
 contiguous; rows of a product's inputs start on 16 bytes (a row stride that is a multiple of 8
-elements). The functions record no autograd graph: gated_ffn_backward returns the gradients. What
-they refuse raises KdError. A device-side wait that exceeds its limit (kd_op_set_timeout; none comes
-near the default of 2 s) ends its kernel early with outputs that are not valid: kd_op_sync waits for
-a stream and raises KdError (KD_ETIMEOUT) then.
+elements). The functions record no autograd graph (gated_ffn_backward returns the gradients): where
+gradients are enabled, tensors that require them are refused; torch.no_grad() or a
+torch.autograd.Function around the calls is the way. An `out` counts as changed in place.
+
+What they refuse raises KdError. A device-side wait that exceeds its limit (kd_op_set_timeout; none
+comes near the default of 2 s) ends its kernel early with outputs that are not valid: kd_op_sync
+waits for a stream and raises KdError (KD_ETIMEOUT) then.
 """
 
 from __future__ import annotations
