@@ -19,9 +19,9 @@ __all__ = ["KdError", "kd_config", "kd_weights", "kd_info", "load_library", "Dec
            "kd_linear_args", "kd_gated_args", "kd_linear", "kd_gated_ffn", "kd_gated_ffn_backward_workspace",
            "kd_gated_ffn_backward", "kd_attention_args", "kd_prompt_attention_workspace",
            "kd_prompt_attention", "kd_op_set_timeout", "kd_op_sync", "kd_op_error",
-           "kd_prefill_workspace", "kd_prefill",
-           "linear", "gated_ffn", "gated_ffn_backward", "prompt_attention"]
+           "kd_prefill_workspace", "kd_prefill"]
 
+# Attributes of the package too, but not in __all__: a star import would import torch for them.
 _OPERATORS = ("linear", "gated_ffn", "gated_ffn_backward", "prompt_attention")
 
 
@@ -33,6 +33,10 @@ def __getattr__(name):
     for n in _OPERATORS:
         globals()[n] = getattr(operators, n)
     return globals()[name]
+
+
+def __dir__():
+    return sorted({*globals(), *_OPERATORS})
 
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkd.so")
