@@ -1,6 +1,7 @@
-"""Build libkd.so in-tree for sm_100a with nvcc, and _kd_torch.so, the operators on torch tensors, with
-g++ against it (no JIT cache)."""
+"""Build libkd.so in-tree for sm_100a with nvcc, and, where torch is installed, _kd_torch.so, the operators on
+torch tensors, with g++ against it and the installed torch (no JIT cache)."""
 
+import importlib.metadata
 import os
 import subprocess
 import sys
@@ -11,6 +12,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libkd.so")
 TORCH_OUT = os.path.join(HERE, "_kd_torch.so")
+TORCH_STAMP = os.path.join(ROOT, "_build", "torch_version")  # the torch that _kd_torch.so was built with
 TORCH_SOURCE = os.path.join(CSRC, "kd_torch.cpp")
 SOURCES = ["kd_kernel.cu", "kd_api.cu", "kd_noalloc.cu", "kd_gemm.cu", "kd_attention.cu",
            "kd_prefill.cu"]
@@ -49,9 +51,27 @@ def _build_lib(force, verbose):
     os.replace(tmp, OUT)
 
 
-def _build_torch(force):
+def _torch_version():
+    """Of the installed torch, without importing it; None without one."""
+    try:
+        return importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        return None
+
+
+def _torch_stale(version):
     deps = [TORCH_SOURCE, os.path.join(ROOT, "include", "kd.h"), os.path.abspath(__file__)]
-    if not force and not _stale(TORCH_OUT, deps):
+    if _stale(TORCH_OUT, deps) or not os.path.exists(TORCH_STAMP):
+        return True
+    with open(TORCH_STAMP) as f:
+        return f.read() != version
+
+
+def _build_torch(force):
+    version = _torch_version()
+    if version is None:  # the C library and its binding need no torch
+        return
+    if not force and not _torch_stale(version):
         return
     import torch
     from torch.utils import cpp_extension
@@ -66,6 +86,9 @@ def _build_torch(force):
                            "-L" + lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
                            "-Wl,-rpath,$ORIGIN"])
     os.replace(tmp, TORCH_OUT)
+    os.makedirs(os.path.dirname(TORCH_STAMP), exist_ok=True)
+    with open(TORCH_STAMP, "w") as f:
+        f.write(version)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
