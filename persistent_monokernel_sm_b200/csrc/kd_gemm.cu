@@ -871,8 +871,10 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant_
 template <bool GATED, typename T, typename O>
 int run_rows(RowArgs g, cudaStream_t stream) {
     // sixteen warps for every SM, as long as a warp of a row still reads its batch
+    int sms = 0;
+    if (int rc = op_sm_count(&sms)) return rc;
     g.share = 1;
-    while (g.share < kRowShare && g.n * g.share < 148 * 16 && g.k >= 256 * 2 * g.share) g.share *= 2;
+    while (g.share < kRowShare && g.n * g.share < sms * 16 && g.k >= 256 * 2 * g.share) g.share *= 2;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)((g.n * g.share + kRowThreads / 32 - 1) / (kRowThreads / 32)));
     cfg.blockDim = dim3(kRowThreads);
