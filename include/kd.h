@@ -287,8 +287,11 @@ typedef struct kd_gated_args {
 int kd_gated_ffn(const kd_gated_args *args, void *h, int64_t ld_h, void *stream);
 
 /* Its gradients for a given dh [m][f]: dx [m][d] (sum of both projections' shares), dwg and dwu
- * [f][d], of the inputs' type; NULL skips one. g and u are recomputed; their gradients are held
- * in the workspace in the inputs' type. m, f >= 1. */
+ * [f][d], of the inputs' type; NULL skips one. g and u are recomputed; their gradients dh u act'(g)
+ * and dh act(g) are held in the workspace in the inputs' type. In fp16 they have its range: past
+ * 65,504 they, and the sums they enter, are infinite or NaN, though the sum of exact terms might be
+ * finite; below 6e-5 they lose precision, below 3e-8 they are 0. All is linear in dh: scale it by a
+ * power of two where that matters. m, f >= 1. */
 size_t kd_gated_ffn_backward_workspace(int64_t m, int64_t f);
 int kd_gated_ffn_backward(const kd_gated_args *args, const void *dh, int64_t ld_dh, void *dx, int64_t ld_dx, void *dwg,
                           int64_t ld_dwg, void *dwu, int64_t ld_dwu, void *workspace, size_t workspace_bytes,
