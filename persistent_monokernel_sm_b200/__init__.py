@@ -382,12 +382,15 @@ class Decoder:
         torch = self.torch
         if max_piece < 1:
             raise KdError(-1, "prefill: max_piece must be at least 1")
+        made_on = torch.cuda.current_stream(self.device)
+        if made_on != self.stream:  # tokens on the GPU belong to it
+            self.stream.wait_stream(made_on)
         with torch.cuda.device(self.device), torch.cuda.stream(self.stream):
             t = torch.as_tensor(tokens, dtype=torch.int32).to(self.device).contiguous()
             n = t.numel()
             nbytes = kd_prefill_workspace(self.cfg, max(1, min(n - 1, max_piece)))
             ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-            self._tokens = t  # kept alive until the stream has passed
+            t.record_stream(self.stream)  # its memory is not used again before the stream has passed
             kd_prefill(self.h, t.data_ptr(), n, kv_len, ws.data_ptr(), nbytes)
         self.pending = 1
 
