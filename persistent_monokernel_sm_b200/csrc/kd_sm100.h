@@ -100,12 +100,17 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const G
     if (mbar_try(bar, parity)) return true;
     return mbar_wait_long(bar, parity, w);
 }
-// A first look at a kernel's first barrier: within a limit that is shorter than a thread may be suspended for,
-// it gives up at once unless the phase has completed.
+// Before a kernel's first wait: with a limit that is shorter than a thread may be suspended for, that wait
+// without a suspension, so that the limit is kept.
 __device__ __forceinline__ bool mbar_first(uint32_t bar, uint32_t parity, const Guard& w) {
-    if (__builtin_expect(w.waits.limit >= kSuspendClocks, 1) || mbar_test(bar, parity)) return true;
-    raise_timeout(w);
-    return false;
+    if (__builtin_expect(w.waits.limit >= kSuspendClocks, 1)) return true;
+    const long long t0 = clock64();
+    while (!mbar_test(bar, parity))
+        if (clock64() - t0 > w.waits.limit) {
+            raise_timeout(w);
+            return false;
+        }
+    return true;
 }
 // The same by all lanes of a warp, with one answer.
 __device__ __forceinline__ bool mbar_wait_all(uint32_t bar, uint32_t parity, const Guard& w) {

@@ -88,6 +88,18 @@ def test_the_limit_belongs_to_the_thread_and_to_the_call(limit):
     assert status() == 0 and torch.equal(got[0], want[0])
 
 
+@pytest.mark.parametrize("name", [n for n in NAMES if "pairs" not in n])
+def test_a_short_limit_that_is_not_exceeded(name, limit):
+    """0.4 ms, where no wait of these calls takes a tenth of it."""
+    run = calls()[name]
+    want = run()
+    torch.cuda.synchronize()
+    limit(400_000)
+    got = run()
+    assert status() == 0
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
 def test_a_limit_of_no_time_is_refused():
     for ns in (0, -1):
         with pytest.raises(kd.KdError) as e:
