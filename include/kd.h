@@ -304,7 +304,8 @@ int kd_gated_ffn_backward(const kd_gated_args *args, const void *dh, int64_t ld_
  * 128; strides count elements, are multiples of 8 and may be in any order (positions before
  * heads too); all four start on 16 bytes. scale is usually 1 / sqrt(head_dim). One token or a
  * long prompt; n may be 0. Cache rows at and after kv_len + n are never used. A position that a
- * token does not see has weight 0 in its sum, so v has to be finite at all kv_len + n.
+ * token does not see has weight 0 in its sum, so v has to be finite at all kv_len + n; a score of
+ * NaN that it does see makes its result NaN.
  * The workspace (device memory, kd_prompt_attention_workspace() bytes for these sizes and head
  * counts, often 0; pointers and strides are not looked at) holds partial results while the
  * call's kernels run; its contents need no preparation. Smaller: KD_ENOMEM. */

@@ -23,11 +23,18 @@
 //
 // What bounds it: for prompts the chain softmax -> P V -> next Q K^T of a stream, 2,900 clocks a
 // pair of blocks where the products alone take 2,048 and the exponentials 2,048 (4,096 tokens, 32/8
-// heads of 128: 122 us, 1.13 PFLOP/s; 16,384: 1.31). A polynomial for a part of the exponentials
-// made it longer (2/8 of them: 130 -> 137 us): the FMA pipe has no room either; so did two threads a
-// row (121 -> 139 us): the exponentials' unit is what a stream's softmax takes. One token: HBM and
-// a fixed 8 us of start, last block and join (32,768 positions, 16/8 heads: 31 us, 4.3 TB/s; 131,072:
-// 88 us, 6.1 TB/s).
+// heads of 128: 124 to 136 us in a graph of eight calls, by the box, 1.0 to 1.1 PFLOP/s; 142 to 145 in
+// a loop of seconds, under the power cap). At head dim 128 the softmax spills 48 bytes a thread. A
+// polynomial for a part of the exponentials made it longer (2/8 of them: 130 -> 137 us): the FMA pipe has
+// no room either; so did two threads a row (121 -> 139 us): the exponentials' unit is what a stream's
+// softmax takes. One token: HBM and a fixed 8 us of start, last block and join (32,768 positions, 16/8
+// heads: 31 us where L2 holds a part of the cache, 37 over three caches in turn, 3.6 TB/s; 131,072: 88 us,
+// 6.1 TB/s).
+//
+// The one pass with a running maximum and sum is the online softmax of Milakov and Gimelshein (2018,
+// arXiv 1805.02867). The tensor cores truncate O's sum towards zero, 9.8e-8 relative for every 16
+// positions where the values have one sign: half a step of fp16 at 80,000 positions of a stream (4,096
+// tokens behind 131,072: 8.6e-4 low), of bf16 at 640,000.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

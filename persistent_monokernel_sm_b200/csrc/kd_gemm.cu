@@ -21,8 +21,10 @@
 //
 // What bounds it: with many tokens the tensor cores (4,096 x 14,336 x 4,096 with both gated
 // projections: 596 us alone, 1.61 of the measured 1.63 PFLOP/s; in a loop of seconds the power cap,
-// 714 us, 1.35 of 1.38); with one token HBM (128,256 x 4,096: 151 us, 7.0 TB/s); between them what a tile costs
-// besides its products: start, ring fill, epilogue, exchange, 3.7 us for the smallest call.
+// 714 us, 1.35 of 1.38); with one token HBM (128,256 x 4,096: 151 us in a graph over two weights in turn,
+// 7.0 TB/s of reads alone, where the measured 6.5 is a copy's; 158 to 177 called one by one, by the box);
+// between them what a tile costs besides its products: start, ring fill, epilogue, exchange, 3.7 us for the
+// smallest call.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdarg.h>
@@ -191,7 +193,10 @@ struct GemmArgs {
 };
 
 // ------------------------------------------------------------------ activations
-// fp32 throughout; silu and its slope by the fast exponential (2 ulp).
+// fp32 throughout. silu and its slope take the fast exponential, which is off by 2 + 1.2 |z| units in the
+// last place: 26 at z = -20, 1.5e-6 of a silu of -4e-8; towards z > 0 it fades, e^-z being small beside 1.
+// gelu's 1 + erf loses its leading digits for z << 0: it is good to 2^-23 |z|, not to digits of a value that
+// is smaller than that.
 template <int ACT>
 __device__ __forceinline__ float act_fn(float z) {
     if constexpr (ACT == KD_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
@@ -893,8 +898,8 @@ int run_rows(RowArgs g, cudaStream_t stream) {
 }
 
 // Whether the row kernel is the quicker one (rows: weight matrices, 1 or 2). One token: at every size
-// measured (us, row kernel and tensor cores: 64 x 64 1.7 / 3.8, 1,536 x 1,536 3.1 / 5.2, 4,096 x 4,096 9.6
-// / 10.5, 128,256 x 4,096 151 / 160). A further token costs it a read and eight products for every 16
+// measured (us in graphs, row kernel and tensor cores: 64 x 64 1.7 / 3.8, 1,536 x 1,536 3.1 / 5.2, 4,096 x 4,096
+// 9.6 / 10.5, 128,256 x 4,096 151 / 160). A further token costs it a read and eight products for every 16
 // bytes of weights, and the tensor cores nothing: two tokens 2,048 x 2,048 4.6 / 5.6, 1,536 x 4,096 6.8 /
 // 6.1; four 1,536 x 1,536 5.2 / 5.4, 2,048 x 2,048 6.0 / 5.7.
 bool few_tokens(int64_t m, int64_t n, int64_t k, int rows) {
@@ -910,9 +915,10 @@ struct Operand {
 
 // Tile width (tokens) and split of the reduction, by an estimate of the time in microseconds.
 // A k-block costs an SM what its instructions or its product take (measured from one-tile
-// runs: 0.20 us up to 64 columns, 0.28 at 128, 0.41 at 256, about linear between), or what the CTAs' loads take at the
-// 10.5 TB/s that L2 was seen to deliver to such tiles, whichever is more; a tile's epilogue runs
-// beside the next tile's products; a split costs its exchange. Both sides, measured (us):
+// runs: 0.20 us up to 64 columns, 0.28 at 128, 0.41 at 256, about linear between), or the CTAs' loads at
+// 10.5 TB/s, whichever is more (fitted to the widths that turned out best; that it is L2's rate is not shown:
+// pairs of CTAs load a quarter less of the gated block of 128 x 2,048 x 8,192, which takes 19 us either way); a
+// tile's epilogue runs beside the next tile's products; a split costs its exchange. Both sides, measured (us):
 // 128 x 4,096 x 2,048: 32 columns 14.1, 128 columns split by four 15.5; 128 x 1,536 x 4,096: 16
 // columns 17.8, 128 split by eight 11.2; 1,024 x 2,048 x 2,048: 128 columns 13.6, 256 19.4.
 struct Plan {
